@@ -307,6 +307,84 @@ COLI_API coli_status coli_moe_stack(const coli_moe_dims* dims, const coli_moe_we
 COLI_API coli_status coli_rmsnorm(int32_t hidden, int32_t T, const float* x, const float* gamma, double eps,
                          float* out, void* stream);
 
+/* 8-bit floating point path.  Codes are e4m3 (4 significant bits, largest 448, NaN 0x7F);
+ * scales are fp32: an activation row has one per 128 columns ([rows][C(cols)], C(n) =
+ * ceil(n / 128)), a weight matrix one per 128 rows and 128 columns ([C(rows)][C(cols)]); the
+ * last block of a row or matrix may be shorter.  A value is code * scale.  Quantisation of
+ * a row v: scale = max |v| over the block / 448 (fp32), code = e4m3(v / scale) (fp32
+ * quotient, to nearest even), all codes 0 where the scale is 0; a block that holds a NaN or
+ * an infinity has a scale of NaN or infinity and NaN codes where its values were not finite
+ * (every code of a block with a NaN).
+ * Products accumulate in fp32: the 128 terms of a scale block on the tensor cores, then
+ * times both scales, block after block in a fixed order (split over several blocks of the
+ * grid where there are few tiles; still one fixed order for given sizes and device).
+ * The fp8 calls share one kind of workspace among themselves; init it with
+ * coli_moe_workspace_init, read errors with coli_moe_read_status (COLI_DEV_BAD_INDEX: lists
+ * outside the batch; what they name is then neither read nor written), and keep calls
+ * that use one workspace in one order (one stream, or events between streams). */
+
+/* Residual addition, RMSNorm and quantisation in one pass:
+ *   s = x + residual, rounded once to dtype (x itself without a residual);  sum = s;
+ *   n = s * gamma / sqrt(mean(s^2) + eps), computed in double and rounded once to fp32;
+ *   out = n;  q, scales = the quantised rows of n.
+ * x, residual, sum [T][hidden] in dtype (residual and sum may be NULL; sum may be x or
+ * residual), gamma [hidden] fp32 or NULL (all ones), out [T][hidden] fp32 or NULL, q
+ * [T][hidden], scales [T][C(hidden)].  hidden a multiple of 16, at most 32768. */
+COLI_API coli_status coli_rmsnorm_fp8(int32_t hidden, int32_t T, const void* x, const void* residual,
+                                      coli_dtype dtype, const float* gamma, double eps, void* sum,
+                                      float* out, uint8_t* q, float* scales, void* stream);
+
+/* Workspace bytes of coli_fp8_matmul (0 for invalid sizes). */
+COLI_API size_t coli_fp8_workspace_bytes(int32_t T, int32_t N, int32_t K);
+
+/* Dense product: y [T][N] (dtype) = residual + x . W^T, rounded once; xq [T][K], xs
+ * [T][C(K)], wq [N][K], wscales [C(N)][C(K)]; residual [T][N] in dtype or NULL, may be y.
+ * K a multiple of 16; any N; T, N, K at most 2^24. */
+COLI_API coli_status coli_fp8_matmul(int32_t T, int32_t N, int32_t K, const uint8_t* xq, const float* xs,
+                                     const uint8_t* wq, const float* wscales, const void* residual,
+                                     void* y, coli_dtype dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of one fp8 expert blob: Gq [I][H] | Uq [I][H] | Dq [H][I] (one byte per weight) |
+ * Gs [C(I)][C(H)] | Us [C(I)][C(H)] | Ds [C(H)][C(I)] (fp32).  0 for invalid sizes. */
+COLI_API size_t coli_moe_blob_bytes_fp8(int32_t hidden, int32_t inter);
+
+/* Workspace bytes of the experts' fp8 calls for batches of up to T_max tokens (0 on invalid
+ * dims). */
+COLI_API size_t coli_moe_workspace_bytes_fp8(const coli_moe_dims* dims, int32_t T_max);
+
+/* The experts' first product over a batch union (lists as from coli_moe_union /
+ * coli_moe_union_restrict; fp8 blobs, expert_stride >= coli_moe_blob_bytes_fp8 and a
+ * multiple of 256; w_router and router_bias are not used):
+ *   hq, hs = the quantised rows of silu(G x) * (U x),
+ * row p of the union positions (the assign order) and row T*k + t for the shared expert:
+ * hq [T*k + T*n_shared][I], hs [..][C(I)].  Rows that the lists leave out stay as they
+ * were.  xq [T][H], xs [T][C(H)].  H and I multiples of 64; any T up to 2^24. */
+COLI_API coli_status coli_moe_gate_up_fp8(const coli_moe_dims* dims, const coli_moe_weights* weights,
+                                          const uint8_t* xq, const float* xs, int32_t T,
+                                          const int32_t* union_ids, const int32_t* n_union,
+                                          const int32_t* offsets, const int32_t* assign, uint8_t* hq,
+                                          float* hs, void* ws, size_t ws_bytes, void* stream);
+
+/* The experts' second product and the combine: y [T][H] fp32 = residual + D_shared h + sum
+ * over slots of w[t][slot] * D_e h, h = (hq, hs) as coli_moe_gate_up_fp8 leaves them.  The
+ * terms of a token are added in slot order; a slot that the lists leave out adds nothing.
+ * residual [T][H] fp32 or NULL, may be y. */
+COLI_API coli_status coli_moe_down_fp8(const coli_moe_dims* dims, const coli_moe_weights* weights,
+                                       const uint8_t* hq, const float* hs, int32_t T, const float* w,
+                                       const int32_t* union_ids, const int32_t* n_union,
+                                       const int32_t* offsets, const int32_t* assign,
+                                       const float* residual, float* y, void* ws, size_t ws_bytes,
+                                       void* stream);
+
+/* Experts and combine for fp8 blobs: coli_moe_gate_up_fp8, then coli_moe_down_fp8, with h
+ * in the workspace. */
+COLI_API coli_status coli_moe_forward_fp8(const coli_moe_dims* dims, const coli_moe_weights* weights,
+                                          const uint8_t* xq, const float* xs, int32_t T, const float* w,
+                                          const int32_t* union_ids, const int32_t* n_union,
+                                          const int32_t* offsets, const int32_t* assign,
+                                          const float* residual, float* y, void* ws, size_t ws_bytes,
+                                          void* stream);
+
 /* Human-readable name of a status code (static string). */
 COLI_API const char* coli_status_string(coli_status s);
 

@@ -29,6 +29,8 @@ EXPORTS = [
     "coli_moe_forward_noalloc", "coli_moe_noalloc_read_status", "coli_debug_wait_timeout",
     "coli_debug_phase_stamps",
     "coli_moe_blob_bytes_fmt", "coli_moe_forward_fmt", "coli_moe_union_restrict",
+    "coli_rmsnorm_fp8", "coli_fp8_workspace_bytes", "coli_fp8_matmul", "coli_moe_blob_bytes_fp8",
+    "coli_moe_workspace_bytes_fp8", "coli_moe_gate_up_fp8", "coli_moe_down_fp8", "coli_moe_forward_fp8",
     "coli_status_string",
 ]
 
@@ -87,6 +89,14 @@ def lib():
                 "coli_moe_blob_bytes_fmt": (sz, [i32, i32, i32]),
                 "coli_moe_union_restrict": (i32, [D, i32, i32, i32, P, P, P, P, P, P, P, P, P]),
                 "coli_moe_forward_fmt": (i32, [D, i32, W, P, i32, P, P, P, P, P, P, P, P, sz, P]),
+                "coli_rmsnorm_fp8": (i32, [i32, i32, P, P, i32, P, ctypes.c_double, P, P, P, P, P]),
+                "coli_fp8_workspace_bytes": (sz, [i32, i32, i32]),
+                "coli_fp8_matmul": (i32, [i32, i32, i32, P, P, P, P, P, P, i32, P, sz, P]),
+                "coli_moe_blob_bytes_fp8": (sz, [i32, i32]),
+                "coli_moe_workspace_bytes_fp8": (sz, [D, i32]),
+                "coli_moe_gate_up_fp8": (i32, [D, W, P, P, i32, P, P, P, P, P, P, P, sz, P]),
+                "coli_moe_down_fp8": (i32, [D, W, P, P, i32, P, P, P, P, P, P, P, P, sz, P]),
+                "coli_moe_forward_fp8": (i32, [D, W, P, P, i32, P, P, P, P, P, P, P, P, sz, P]),
                 "coli_status_string": (ctypes.c_char_p, [i32]),
             }
             for name, (res, args) in sig.items():
@@ -262,6 +272,51 @@ def coli_moe_stack(dims, layers, gammas, eps, x, T, idx, y, ws, stream=None) -> 
 
 def coli_rmsnorm(hidden, T, x, gamma, eps, out, stream=None) -> int:
     return lib().coli_rmsnorm(hidden, T, _p(x), _p(gamma), float(eps), _p(out), _s(stream))
+
+
+# 8-bit floating point path: codes are torch.float8_e4m3fn (or uint8) tensors, scales fp32.
+
+def coli_rmsnorm_fp8(hidden, T, x, residual, gamma, eps, sum, out, q, scales, stream=None) -> int:
+    return lib().coli_rmsnorm_fp8(hidden, T, _p(x), _p(residual), _dt(x), _p(gamma), float(eps), _p(sum), _p(out),
+                                  _p(q), _p(scales), _s(stream))
+
+
+def coli_fp8_workspace_bytes(T: int, N: int, K: int) -> int:
+    return lib().coli_fp8_workspace_bytes(T, N, K)
+
+
+def coli_fp8_matmul(T, N, K, xq, xs, wq, wscales, residual, y, ws, stream=None) -> int:
+    return lib().coli_fp8_matmul(T, N, K, _p(xq), _p(xs), _p(wq), _p(wscales), _p(residual), _p(y), _dt(y), _p(ws),
+                                 ws.numel(), _s(stream))
+
+
+def coli_moe_blob_bytes_fp8(hidden: int, inter: int) -> int:
+    return lib().coli_moe_blob_bytes_fp8(hidden, inter)
+
+
+def coli_moe_workspace_bytes_fp8(dims: Dims, T_max: int) -> int:
+    return lib().coli_moe_workspace_bytes_fp8(ctypes.byref(dims), T_max)
+
+
+def coli_moe_gate_up_fp8(dims, weights, xq, xs, T, union_ids, n_union, offsets, assign, hq, hs, ws,
+                         stream=None) -> int:
+    return lib().coli_moe_gate_up_fp8(ctypes.byref(dims), ctypes.byref(weights), _p(xq), _p(xs), T, _p(union_ids),
+                                      _p(n_union), _p(offsets), _p(assign), _p(hq), _p(hs), _p(ws), ws.numel(),
+                                      _s(stream))
+
+
+def coli_moe_down_fp8(dims, weights, hq, hs, T, w, union_ids, n_union, offsets, assign, residual, y, ws,
+                      stream=None) -> int:
+    return lib().coli_moe_down_fp8(ctypes.byref(dims), ctypes.byref(weights), _p(hq), _p(hs), T, _p(w),
+                                   _p(union_ids), _p(n_union), _p(offsets), _p(assign), _p(residual), _p(y), _p(ws),
+                                   ws.numel(), _s(stream))
+
+
+def coli_moe_forward_fp8(dims, weights, xq, xs, T, w, union_ids, n_union, offsets, assign, residual, y, ws,
+                         stream=None) -> int:
+    return lib().coli_moe_forward_fp8(ctypes.byref(dims), ctypes.byref(weights), _p(xq), _p(xs), T, _p(w),
+                                      _p(union_ids), _p(n_union), _p(offsets), _p(assign), _p(residual), _p(y),
+                                      _p(ws), ws.numel(), _s(stream))
 
 
 # ------------------------------------------------------------------------------------

@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "fused.cuh"
 #include "fmt.cuh"
+#include "fp8.cuh"
 #include "gemm.cuh"
 #include "gemv.cuh"
 #include "rmsnorm.cuh"
@@ -628,4 +629,233 @@ coli_status coli_moe_forward_fmt(const coli_moe_dims* dims, int32_t fmt, const c
     f.y = y;
     f.status = reinterpret_cast<uint32_t*>(ws);
     return cuda_status(fmt_forward_launch(f, di.sms, (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------------------
+// 8-bit floating point path
+// ---------------------------------------------------------------------------------------
+namespace {
+
+constexpr int32_t kFp8MaxTokens = 1 << 24, kFp8MaxCols = 1 << 24;
+
+struct Fp8Layout {
+    size_t hq, hs, scratch, total;
+};
+
+// header and counters | h codes | h scales | scratch of the larger product
+Fp8Layout fp8_layout(const coli_moe_dims* d, int64_t T)
+{
+    Fp8Layout L;
+    const size_t rows = (size_t)T * (d->top_k + d->n_shared);
+    size_t off = up(sizeof(WsHeader) + kCntBytes, kAlign);
+    L.hq = off;
+    off = up(off + rows * d->inter, kAlign);
+    L.hs = off;
+    off = up(off + rows * fp8_blocks(d->inter) * sizeof(float), kAlign);
+    L.scratch = off;
+    const size_t gu = fp8_scratch_bytes(FP8_GATE_UP, T, d->hidden, d->top_k, d->n_shared);
+    const size_t dn = fp8_scratch_bytes(FP8_DOWN, T, d->hidden, d->top_k, d->n_shared);
+    L.total = up(off + (gu > dn ? gu : dn), kAlign);
+    return L;
+}
+
+size_t fp8_dense_bytes(int64_t T)
+{
+    return up(up(sizeof(WsHeader) + kCntBytes, kAlign) + fp8_scratch_bytes(FP8_DENSE, T, 0, 0, 0), kAlign);
+}
+
+static_assert(kFp8Ctas <= kCntWords, "a counter per CTA of a split product");
+
+void fp8_args(Fp8ProductArgs& a, int mode, int32_t T, void* ws, size_t scratch, int sms)
+{
+    memset(&a, 0, sizeof(a));
+    a.mode = mode;
+    a.T = T;
+    a.status = reinterpret_cast<uint32_t*>(ws);
+    a.tickets = reinterpret_cast<uint32_t*>((uint8_t*)ws + sizeof(WsHeader));
+    a.scratch = (uint8_t*)ws + scratch;
+    a.num_sms = sms;
+}
+
+void fp8_expert_args(Fp8ProductArgs& a, const coli_moe_dims* d, const coli_moe_weights* w,
+                     const int32_t* union_ids, const int32_t* n_union, const int32_t* offsets,
+                     const int32_t* assign)
+{
+    a.H = d->hidden;
+    a.I = d->inter;
+    a.E = d->n_experts;
+    a.k = d->top_k;
+    a.n_shared = d->n_shared;
+    a.experts = w->experts;
+    a.stride = w->expert_stride;
+    a.shared = w->shared;
+    a.union_ids = union_ids;
+    a.n_union = n_union;
+    a.offsets = offsets;
+    a.assign = assign;
+}
+
+// Checks common to the experts' products; COLI_OK to go on.
+coli_status fp8_moe_check(const coli_moe_dims* d, const coli_moe_weights* w, int32_t T,
+                          const int32_t* union_ids, const int32_t* n_union, const int32_t* offsets,
+                          const int32_t* assign, void* ws, size_t ws_bytes)
+{
+    if (!w || !w->experts || !aligned16(w->experts) || (d->n_shared && (!w->shared || !aligned16(w->shared))) ||
+        w->expert_stride < fp8_blob_bytes(d->hidden, d->inter) || w->expert_stride % 256)
+        return COLI_EINVAL;
+    if (!union_ids || !n_union || !offsets || !assign) return COLI_EINVAL;
+    if (T > kFp8MaxTokens || d->hidden > kFp8MaxCols || d->inter > kFp8MaxCols) return COLI_EUNSUPPORTED;
+    if (!ws || !aligned16(ws)) return COLI_EINVAL;
+    if (ws_bytes < fp8_layout(d, T).total) return COLI_ENOMEM;
+    return COLI_OK;
+}
+
+}  // namespace
+
+coli_status coli_rmsnorm_fp8(int32_t hidden, int32_t T, const void* x, const void* residual,
+                             coli_dtype dtype, const float* gamma, double eps, void* sum, float* out,
+                             uint8_t* q, float* scales, void* stream)
+{
+    if (hidden <= 0 || hidden % 16 || T < 0 || !(eps >= 0.0) || (dtype != COLI_F32 && dtype != COLI_BF16))
+        return COLI_EINVAL;
+    if (T == 0) return COLI_OK;
+    if (!x || !q || !scales || !aligned16(x) || !aligned16(q) || !aligned16(scales) ||
+        (residual && !aligned16(residual)) || (gamma && !aligned16(gamma)) || (sum && !aligned16(sum)) ||
+        (out && !aligned16(out)))
+        return COLI_EINVAL;
+    if (hidden > kFp8NormMaxHidden) return COLI_EUNSUPPORTED;
+    DevInfo di;
+    if (!dev_info(di)) return COLI_ECUDA;
+    Fp8NormParams p;
+    memset(&p, 0, sizeof(p));
+    p.H = hidden;
+    p.T = T;
+    p.bf16 = dtype == COLI_BF16;
+    p.x = x;
+    p.residual = residual;
+    p.gamma = gamma;
+    p.eps = eps;
+    p.sum = sum;
+    p.out = out;
+    p.q = q;
+    p.scales = scales;
+    return cuda_status(fp8_norm_launch(p, di.sms, (cudaStream_t)stream));
+}
+
+size_t coli_fp8_workspace_bytes(int32_t T, int32_t N, int32_t K)
+{
+    if (T < 0 || N < 1 || K < 16 || K % 16) return 0;
+    return fp8_dense_bytes(T);
+}
+
+coli_status coli_fp8_matmul(int32_t T, int32_t N, int32_t K, const uint8_t* xq, const float* xs,
+                            const uint8_t* wq, const float* wscales, const void* residual, void* y,
+                            coli_dtype dtype, void* ws, size_t ws_bytes, void* stream)
+{
+    if (T < 0 || N < 1 || K < 16 || K % 16 || (dtype != COLI_F32 && dtype != COLI_BF16)) return COLI_EINVAL;
+    if (T == 0) return COLI_OK;
+    if (!xq || !xs || !wq || !wscales || !y || !aligned16(xq) || !aligned16(xs) || !aligned16(wq) ||
+        !aligned16(wscales) || !aligned16(y) || (residual && !aligned16(residual)))
+        return COLI_EINVAL;
+    if (T > kFp8MaxTokens || N > kFp8MaxCols || K > kFp8MaxCols) return COLI_EUNSUPPORTED;
+    if (!ws || !aligned16(ws)) return COLI_EINVAL;
+    if (ws_bytes < fp8_dense_bytes(T)) return COLI_ENOMEM;
+    DevInfo di;
+    if (!dev_info(di)) return COLI_ECUDA;
+    Fp8ProductArgs a;
+    fp8_args(a, FP8_DENSE, T, ws, up(sizeof(WsHeader) + kCntBytes, kAlign), di.sms);
+    a.N = N;
+    a.K = K;
+    a.w = wq;
+    a.wscale = wscales;
+    a.x = xq;
+    a.xs = xs;
+    a.residual = residual;
+    a.y = y;
+    a.y_bf16 = dtype == COLI_BF16;
+    return cuda_status(fp8_product_launch(a, (cudaStream_t)stream));
+}
+
+size_t coli_moe_blob_bytes_fp8(int32_t hidden, int32_t inter)
+{
+    if (hidden < 64 || inter < 64 || hidden % 64 || inter % 64) return 0;
+    return fp8_blob_bytes(hidden, inter);
+}
+
+size_t coli_moe_workspace_bytes_fp8(const coli_moe_dims* dims, int32_t T_max)
+{
+    if (!dims_ok(dims) || T_max < 0) return 0;
+    return fp8_layout(dims, T_max).total;
+}
+
+coli_status coli_moe_gate_up_fp8(const coli_moe_dims* dims, const coli_moe_weights* weights,
+                                 const uint8_t* xq, const float* xs, int32_t T, const int32_t* union_ids,
+                                 const int32_t* n_union, const int32_t* offsets, const int32_t* assign,
+                                 uint8_t* hq, float* hs, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!dims_ok(dims) || T < 0) return COLI_EINVAL;
+    if (T == 0) return COLI_OK;
+    if (!xq || !xs || !hq || !hs || !aligned16(xq) || !aligned16(xs) || !aligned16(hq) || !aligned16(hs))
+        return COLI_EINVAL;
+    const coli_status st = fp8_moe_check(dims, weights, T, union_ids, n_union, offsets, assign, ws, ws_bytes);
+    if (st != COLI_OK) return st;
+    DevInfo di;
+    if (!dev_info(di)) return COLI_ECUDA;
+    Fp8ProductArgs a;
+    fp8_args(a, FP8_GATE_UP, T, ws, fp8_layout(dims, T).scratch, di.sms);
+    fp8_expert_args(a, dims, weights, union_ids, n_union, offsets, assign);
+    a.x = xq;
+    a.xs = xs;
+    a.hq = hq;
+    a.hs = hs;
+    return cuda_status(fp8_product_launch(a, (cudaStream_t)stream));
+}
+
+coli_status coli_moe_down_fp8(const coli_moe_dims* dims, const coli_moe_weights* weights,
+                              const uint8_t* hq, const float* hs, int32_t T, const float* w,
+                              const int32_t* union_ids, const int32_t* n_union, const int32_t* offsets,
+                              const int32_t* assign, const float* residual, float* y, void* ws,
+                              size_t ws_bytes, void* stream)
+{
+    if (!dims_ok(dims) || T < 0) return COLI_EINVAL;
+    if (T == 0) return COLI_OK;
+    if (!hq || !hs || !w || !y || !aligned16(hq) || !aligned16(hs) || !aligned16(y) ||
+        (residual && !aligned16(residual)))
+        return COLI_EINVAL;
+    const coli_status st = fp8_moe_check(dims, weights, T, union_ids, n_union, offsets, assign, ws, ws_bytes);
+    if (st != COLI_OK) return st;
+    DevInfo di;
+    if (!dev_info(di)) return COLI_ECUDA;
+    Fp8ProductArgs a;
+    fp8_args(a, FP8_DOWN, T, ws, fp8_layout(dims, T).scratch, di.sms);
+    fp8_expert_args(a, dims, weights, union_ids, n_union, offsets, assign);
+    a.x = hq;
+    a.xs = hs;
+    a.wts = w;
+    a.residual = residual;
+    a.y = y;
+    return cuda_status(fp8_product_launch(a, (cudaStream_t)stream));
+}
+
+coli_status coli_moe_forward_fp8(const coli_moe_dims* dims, const coli_moe_weights* weights,
+                                 const uint8_t* xq, const float* xs, int32_t T, const float* w,
+                                 const int32_t* union_ids, const int32_t* n_union, const int32_t* offsets,
+                                 const int32_t* assign, const float* residual, float* y, void* ws,
+                                 size_t ws_bytes, void* stream)
+{
+    if (!dims_ok(dims) || T < 0) return COLI_EINVAL;
+    if (T == 0) return COLI_OK;
+    if (!xq || !xs || !w || !y || !aligned16(xq) || !aligned16(xs) || !aligned16(y) ||
+        (residual && !aligned16(residual)))
+        return COLI_EINVAL;
+    coli_status st = fp8_moe_check(dims, weights, T, union_ids, n_union, offsets, assign, ws, ws_bytes);
+    if (st != COLI_OK) return st;
+    const Fp8Layout L = fp8_layout(dims, T);
+    uint8_t* hq = (uint8_t*)ws + L.hq;
+    float* hs = reinterpret_cast<float*>((uint8_t*)ws + L.hs);
+    st = coli_moe_gate_up_fp8(dims, weights, xq, xs, T, union_ids, n_union, offsets, assign, hq, hs, ws, ws_bytes,
+                              stream);
+    if (st != COLI_OK) return st;
+    return coli_moe_down_fp8(dims, weights, hq, hs, T, w, union_ids, n_union, offsets, assign, residual, y, ws,
+                             ws_bytes, stream);
 }

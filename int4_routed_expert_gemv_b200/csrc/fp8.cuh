@@ -1,0 +1,74 @@
+// 8-bit floating point path (e4m3 codes, fp32 scales per block of 128): host-visible
+// descriptions of the norm that quantises and of the block-scaled products.
+//
+// Scales: an activation row has one per 128 columns ([rows][ceil(cols / 128)]), a weight
+// matrix one per 128 rows and 128 columns ([ceil(rows / 128)][ceil(cols / 128)]).
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace coli {
+
+constexpr int kFp8Block = 128;
+constexpr float kFp8Max = 448.0f;     // largest e4m3 value
+constexpr int kFp8Ctas = 148;         // CTAs of a product launch at most (one per SM)
+
+__host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// Bytes of one expert blob: Gq | Uq | Dq (one byte per weight) | Gs | Us | Ds (fp32).
+inline size_t fp8_blob_bytes(int H, int I)
+{
+    return 3 * (size_t)H * I + 3 * sizeof(float) * (size_t)fp8_blocks(H) * fp8_blocks(I);
+}
+
+constexpr int kFp8NormMaxHidden = 32768;
+
+struct Fp8NormParams {
+    int H, T, bf16;
+    const void* x;          // [T][H] fp32 or bf16
+    const void* residual;   // [T][H] same type, or null
+    const float* gamma;     // [H], or null for ones
+    double eps;
+    void* sum;              // [T][H] same type, or null
+    float* out;             // [T][H], or null
+    uint8_t* q;             // [T][H]
+    float* scales;          // [T][blocks]
+};
+cudaError_t fp8_norm_launch(const Fp8NormParams& p, int num_sms, cudaStream_t s);
+
+enum Fp8Mode : int { FP8_DENSE = 0, FP8_GATE_UP = 1, FP8_DOWN = 2 };
+
+// One block-scaled product.  DENSE: y [T][N] from x [T][K] and w [N][K].  GATE_UP / DOWN:
+// over the union lists and the shared expert, K = H or I.
+struct Fp8ProductArgs {
+    int mode;
+    int T, N, K;                 // DENSE
+    const uint8_t* w;            // DENSE
+    const float* wscale;         // DENSE
+    int H, I, E, k, n_shared;    // experts
+    const uint8_t* experts;
+    uint64_t stride;
+    const uint8_t* shared;
+    const uint8_t* x;            // codes: [T][K], or h [T*k + T*n_shared][I] for DOWN
+    const float* xs;             // their scales
+    const int32_t* union_ids;
+    const int32_t* n_union;
+    const int32_t* offsets;
+    const int32_t* assign;
+    const float* wts;            // DOWN: routing weights [T][k]
+    const void* residual;        // DENSE (y's type) / DOWN (fp32), or null
+    void* y;                     // DENSE: [T][N] fp32 or bf16; DOWN: [T][H] fp32
+    int y_bf16;                  // DENSE
+    uint8_t* hq;                 // GATE_UP: [rows][I]
+    float* hs;                   // GATE_UP: [rows][blocks of I]
+    uint32_t* status;            // workspace header
+    uint32_t* tickets;           // kFp8Ctas counters, zero between launches
+    uint8_t* scratch;            // fp8_scratch_bytes()
+    int num_sms;
+};
+// Scratch of one product: partial tiles, and for DOWN the rows before the combine.
+size_t fp8_scratch_bytes(int mode, int64_t T, int H, int k, int n_shared);
+cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s);
+
+}  // namespace coli
