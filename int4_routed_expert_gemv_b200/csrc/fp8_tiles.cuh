@@ -1,0 +1,295 @@
+// Pieces shared by the two kernels of the e4m3 products (fp8_decode.cu, fp8_pair.cu): the
+// launch's parameters, groups of tokens, the schedule of tiles, tensor-core wrappers.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "fp8.cuh"
+#include "tcgen05.cuh"
+
+namespace coli {
+namespace fp8 {
+
+constexpr int kM = 128;                 // weight rows of a CTA's MMA operand
+constexpr int kThreads = 384;
+constexpr int kEpi = 256;               // threads of the two accumulating warpgroups
+constexpr int kSlots = 8;               // ring of scale products
+constexpr int kMaxGroups = 1024 + 1;    // experts and the shared one
+
+// Parameters of a launch.
+struct Params {
+    CUtensorMap w[2];             // dense or routed experts, shared expert
+    CUtensorMap x;
+    int K, kb;                    // contraction length and its scale blocks
+    int rows, rb;                 // output rows of a matrix, 256-row (or gate/up pair) blocks
+    int T, k, E, n_shared, I;
+    int row_off;                  // rows before the wanted matrix inside a blob's map
+    const float* ws[2];           // dense: scales; experts: first blob's scales, shared's
+    uint64_t ws_stride;           // bytes between experts' scales
+    const float* xs;
+    const int32_t* union_ids;
+    const int32_t* n_union;
+    const int32_t* offsets;
+    const int32_t* assign;
+    const void* residual;
+    void* y;
+    int y_bf16;
+    uint8_t* hq;
+    float* hs;
+    float* z;                     // DOWN: [T*k + T*n_shared][rows]
+    uint8_t* present;             // DOWN: [T*k] 1 where z has the row
+    float* partial;               // sums of the parts of split tiles
+    uint32_t* tickets;            // parts that have arrived, by the first part's worker
+    uint32_t* status;
+};
+
+// kind::f8f6f4 instruction descriptor: e4m3 A and B, fp32 D, both K-major, M x N.
+__device__ __forceinline__ uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a));
+}
+
+// Group g of a product: the shared expert first (the longest), then the union.
+struct Group {
+    int expert;   // -1: shared
+    int base;     // first row (position in the union lists; T*k + t for the shared expert)
+    int count;    // 0 where the lists are not a batch union's: nothing of them is read or written
+    bool bad;
+};
+
+template <int MODE>
+__device__ __forceinline__ Group group_of(const Params& p, int g)
+{
+    Group v;
+    v.bad = false;
+    if (MODE == FP8_DENSE) {
+        v.expert = 0;
+        v.base = 0;
+        v.count = p.T;
+    } else if (g < p.n_shared) {
+        v.expert = -1;
+        v.base = p.T * p.k;
+        v.count = p.T;
+    } else {
+        const int u = g - p.n_shared;
+        v.expert = p.union_ids[u];
+        v.base = p.offsets[u];
+        const int end = p.offsets[u + 1];
+        v.bad = v.expert < 0 || v.expert >= p.E || v.base < 0 || end < v.base || end > p.T * p.k;
+        v.count = v.bad ? 0 : end - v.base;
+        if (v.bad) v.expert = v.base = 0;
+    }
+    return v;
+}
+
+// Token of row `pos` of the union lists (-1: not a position of this batch).
+__device__ __forceinline__ int position_of(const Params& p, int pos)
+{
+    const int a = p.assign[pos];
+    return a < 0 || a >= p.T * p.k ? -1 : a;
+}
+
+struct Item {
+    int tile, kb0, kb1;
+};
+
+// The items of worker c of G (a CTA or a pair): a run of K steps over the first `split` tiles,
+// then whole tiles.  `least`: K steps of a run at least, so that the parts of a tile, which
+// one worker adds up, stay few.
+struct Schedule {
+    int tiles, split, kb, G, c;
+    int per, more, n_run;         // units per run, runs with one more, runs
+    int u, u1, t;
+
+    __device__ void init(int tiles_, int kb_, int G_, int c_, int least)
+    {
+        tiles = tiles_;
+        kb = kb_;
+        G = G_;
+        c = c_;
+        const int rest = tiles % G;
+        split = rest == 0 ? 0 : tiles < G ? tiles : rest + G;
+        const int units = split * kb;
+        n_run = min(G, max(1, units / least));
+        per = units / n_run;
+        more = units - per * n_run;
+        u = start(min(c, n_run));
+        u1 = start(min(c + 1, n_run));
+        t = split + c;
+    }
+    __device__ int start(int cc) const { return cc >= n_run ? split * kb : cc * per + min(cc, more); }
+    __device__ int owner(int unit) const
+    {
+        const int big = more * (per + 1);
+        return unit < big ? unit / (per + 1) : more + (unit - big) / max(per, 1);
+    }
+    __device__ bool next(Item& it)
+    {
+        if (u < u1) {
+            it.tile = u / kb;
+            it.kb0 = u - it.tile * kb;
+            it.kb1 = min(kb, it.kb0 + u1 - u);
+            u += it.kb1 - it.kb0;
+            return true;
+        }
+        if (t < tiles) {
+            it.tile = t;
+            it.kb0 = 0;
+            it.kb1 = kb;
+            t += G;
+            return true;
+        }
+        return false;
+    }
+};
+
+// Where a tile lies: its group, first token of the group, tokens, row block.
+struct Tile {
+    Group g;
+    int t0, n, rb;
+};
+
+// first[g]: tiles of nt tokens before group g.
+template <int MODE>
+__device__ __forceinline__ Tile tile_of(const Params& p, const int* first, int n_groups, int nt, int tile)
+{
+    Tile v;
+    const int q = tile / p.rb;
+    v.rb = tile - q * p.rb;
+    int lo = 0, hi = n_groups;                 // last group with first[g] <= q
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= q) lo = mid;
+        else hi = mid;
+    }
+    v.g = group_of<MODE>(p, lo);
+    v.t0 = (q - first[lo]) * nt;
+    v.n = min(nt, v.g.count - v.t0);
+    return v;
+}
+
+// One warp: first[] of every group, the groups and the tiles.
+template <int MODE>
+__device__ __forceinline__ void plan_tiles(const Params& p, int nt, int lane, int* first, int* n_groups, int* tiles)
+{
+    int ng = 1;
+    if (MODE != FP8_DENSE) {
+        const int nu = *p.n_union;
+        if ((nu < 0 || nu > p.E) && lane == 0) set_flag(p.status, DEV_BAD_INDEX);
+        ng = p.n_shared + min(max(nu, 0), p.E);
+    }
+    int base = 0;
+    for (int g0 = 0; g0 < ng; g0 += 32) {
+        const int g = g0 + lane;
+        int n = 0;
+        if (g < ng) {
+            const Group v = group_of<MODE>(p, g);
+            if (v.bad) set_flag(p.status, DEV_BAD_INDEX);
+            n = (v.count + nt - 1) / nt;
+        }
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += v;
+        }
+        if (g < ng) first[g] = base + x - n;
+        base += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+        *n_groups = ng;
+        *tiles = base * p.rb;
+    }
+}
+
+// Warp that forms the scale products of a ring slot: columns lane, lane + 32, .. below NT
+// (xrow[l]: a column's scales, null for a column without a token) times W weight scales.
+// K steps are fetched B at a time, one batch ahead.
+template <int NT, int W, int B>
+struct ScaleWarp {
+    static constexpr int L = (NT + 31) / 32;
+    const float* xrow[L];
+    const float* w[W];
+
+    __device__ __forceinline__ void run(const Item& it, int lane, float* ring, uint64_t* full, uint64_t* empty,
+                                        uint32_t& n, bool& dead, uint32_t* status, uint32_t site)
+    {
+        float xv[B][L], wv[B][W];
+        auto fetch = [&](int kb) {
+#pragma unroll
+            for (int i = 0; i < B; i++) {
+                const bool in = kb + i < it.kb1;
+#pragma unroll
+                for (int l = 0; l < L; l++) xv[i][l] = in && xrow[l] ? __ldg(xrow[l] + kb + i) : 0.0f;
+#pragma unroll
+                for (int m = 0; m < W; m++) wv[i][m] = in && w[m] ? __ldg(w[m] + kb + i) : 0.0f;
+            }
+        };
+        fetch(it.kb0);
+        for (int kb = it.kb0; kb < it.kb1; kb += B) {
+            float s[B][W][L];
+#pragma unroll
+            for (int i = 0; i < B; i++)
+#pragma unroll
+                for (int m = 0; m < W; m++)
+#pragma unroll
+                    for (int l = 0; l < L; l++) s[i][m][l] = xv[i][l] * wv[i][m];
+            if (kb + B < it.kb1) fetch(kb + B);
+#pragma unroll
+            for (int i = 0; i < B; i++) {
+                if (kb + i >= it.kb1) break;
+                const int slot = n % kSlots;
+                if (!dead && !mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, status, site)) dead = true;
+                float* d = ring + slot * W * NT;
+#pragma unroll
+                for (int m = 0; m < W; m++)
+#pragma unroll
+                    for (int l = 0; l < L; l++)
+                        if (lane + 32 * l < NT) d[m * NT + lane + 32 * l] = s[i][m][l];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[slot]);
+                n++;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Code of v at a scale (0 at scale 0).
+__device__ __forceinline__ uint8_t code_of(float v, float scale)
+{
+    return (uint8_t)__nv_cvt_float_to_fp8(scale != 0.0f ? __fdiv_rn(v, scale) : 0.0f, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+}  // namespace fp8
+
+// One launch of a product: for at most 16 tokens, and for more.
+cudaError_t fp8_decode_launch(int mode, const fp8::Params& p, int num_sms, cudaStream_t s);
+cudaError_t fp8_pair_launch(int mode, const fp8::Params& p, int num_sms, cudaStream_t s);
+
+}  // namespace coli
