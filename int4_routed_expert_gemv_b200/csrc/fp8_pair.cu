@@ -78,37 +78,13 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void arrive_cluster(uint32_t bar)
+// Arrival on a barrier of either CTA (a shared::cluster address).  What these barriers hand
+// over is tensor memory and tiles that TMA and the MMAs touch, ordered by their own
+// completion and the tcgen05 fences, so the arrival carries no cluster-wide release (a
+// release there costs a fence of the thread's global accesses, 1500 cycles a K step).
+__device__ __forceinline__ void arrive_pair(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// mbar_wait for arrivals from the other CTA of the pair.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t site)
-{
-    if (try_wait_cluster(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (true) {
-        if (try_wait_cluster(bar, parity)) return true;
-        if (clock64() - t0 > kWaitBudgetCycles) {
-            set_flag(status, DEV_TIMEOUT);
-            atomicExch(status + 3, site);
-            return false;
-        }
-    }
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Loads into this CTA that complete on a barrier of rank 0 (a shared::cluster address).
@@ -281,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int row0 = (MODE == FP8_DENSE ? tl.t0 : tl.g.base + tl.t0) + rank * kM;
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int s = n % kStages;
-                    if (!dead && !wait_cluster(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
+                    if (!dead && !mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
                     if (dead) continue;
                     uint8_t* st = smem + (size_t)s * kStage;
                     const uint32_t bar = map_to(&full[s], 0);
@@ -301,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t last = n < (uint32_t)kStages ? n : (uint32_t)kStages;
                 for (uint32_t i = 0; i < last; i++) {
                     const uint32_t m = n - 1 - i;
-                    wait_cluster(&full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
+                    mbar_wait(&full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
                 }
             }
         } else if (warp == 9) {
@@ -312,8 +288,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 while (sch.next(it)) {
                     for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                         const int s = n % kStages, b = n % kBufs;
-                        if (!dead && !wait_cluster(&acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
-                        if (!dead && !wait_cluster(&full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
+                        if (!dead && !mbar_wait(&acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
+                        if (!dead && !mbar_wait(&full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
                         tc_fence_after();
                         if (!dead) {
                             const uint8_t* st = smem + (size_t)s * kStage;
@@ -327,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 commit_pair(mma_done);
-                wait_cluster(mma_done, 0, p.status, kSite + 5);
+                mbar_wait(mma_done, 0, p.status, kSite + 5);
             }
         }
     } else {
@@ -402,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_cluster(ae + b * 8);
+                    if (lane == 0) arrive_pair(ae + b * 8);
                     scaled_add(acc + 48, v1, pk2f(sb, sb));
                 }
             } else {
@@ -411,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int b = n % kBufs;
                     if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
                     __syncwarp();
-                    if (lane == 0) arrive_cluster(ae + b * 8);
+                    if (lane == 0) arrive_pair(ae + b * 8);
                 }
             }
             if (it.kb1 - it.kb0 < p.kb) {
