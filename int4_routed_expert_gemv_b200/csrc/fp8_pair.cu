@@ -11,15 +11,16 @@
 // weights there, the scales of all columns come from shared memory, and those reads, beside
 // the MMA's own, took 3 times as long as everything else.
 //
-// The two row blocks of a tile: DENSE and DOWN neighbours (warpgroup g has block g), GATE_UP
-// the gate and the up rows of the same 128 intermediate columns, which are one scale block of
-// h (warpgroup g has columns 64 g .. of both).
+// The two row blocks of a tile: DENSE and DOWN neighbours, GATE_UP the gate and the up rows of
+// the same 128 intermediate columns, which are one scale block of h.  Warpgroup g has columns
+// 64 g .. of both.
 //
-// CTA, 10 warps of use in 12:
+// CTA, 12 warps:
 //   warps 0-7   two warpgroups: scaled accumulation, outputs
-//   warp 8      TMA producer of this CTA's tokens (rows one after another, or gathered by the
-//               union lists) and weight rows
+//   warp 8      TMA producer of this CTA's weight rows and, where they lie one after another,
+//               tokens
 //   warp 9      tensor memory; in rank 0 the pair's single-thread tcgen05.mma issuer
+//   warps 10-11 GATE_UP: copies of the tokens that the union lists name
 // A part of a split tile goes to the workspace; the last one to arrive adds the parts up in
 // K order (Schedule).
 #include <string.h>
@@ -36,14 +37,16 @@ constexpr int NT = 256;                           // tokens of a tile
 constexpr int C = 128;                            // columns of a thread
 constexpr uint32_t kTile = kM * 128;              // bytes of a CTA's tokens or weights per K step
 constexpr uint32_t kStage = 2 * kTile;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kBufs = 2;
 constexpr uint32_t kTmem = kBufs * 256;
 constexpr int kBox = 64;                          // rows of a token box
 constexpr int kLeast = 6;                         // K steps of a run at least
-constexpr int kPad = 20;                          // floats of a staged row: 16 and a gap
-constexpr size_t kOut = (size_t)(kEpi / 32) * 32 * kPad * 4;
-constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 2 * kM * 4 + (kMaxGroups + 3) / 4 * 4 * 4 + 16 + 256;
+constexpr int kPitch = 144;                       // bytes of a staged row: 128 and a gap
+constexpr size_t kOut = (size_t)kEpi * kPitch;
+constexpr int kGatherWarps = 2, kGatherLag = 3;   // warps that gather tokens, and how many K steps they run ahead
+constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 2 * kM * 4 + 2 * kM * 4 +
+                         (kMaxGroups + 3) / 4 * 4 * 4 + 16 + 256;
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -106,14 +109,10 @@ __device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, 
         : "memory");
 }
 
-// Four rows of a 2-D map (box one row high) into four consecutive 128-byte rows.
-__device__ __forceinline__ void pair_gather4(void* dst, const CUtensorMap* map, int x, int4 y, uint32_t bar)
+// 16 bytes global -> shared, zeros where `in` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar)
-        : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -157,21 +156,103 @@ __device__ __forceinline__ void scaled_add(uint64_t* acc, const uint32_t (&v)[32
     for (int j = 0; j < 32; j += 2) acc[j / 2] = ffma2(pk2(v[j], v[j + 1]), s, acc[j / 2]);
 }
 
-// 16 columns of a warp's 32 rows, from a thread's own row to rows written side by side: calls
-// put(row, column, float4) with 4 consecutive columns.
-template <class Put>
-__device__ __forceinline__ void through_smem(float* stage, const float* v, int lane, Put put)
+__device__ __forceinline__ float acc_at(const uint64_t (&acc)[C / 2], int j)
 {
+    const float2 f = unpk2(acc[j / 2]);
+    return j & 1 ? f.y : f.x;
+}
+
+// A warp's 32 rows of outputs, one per thread (orow: its row of y, -1 for none): two runs of 64
+// columns, at c0 and c0 + 128, plus the residual, rounded once.  Rows go through shared
+// memory, 128 bytes each at a time, so that 8 neighbouring lanes write (and read the
+// residual's) 128 consecutive bytes; the loads of a piece are under way together.
+template <class Y>
+__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, uint64_t (&acc)[C / 2],
+                                           uint8_t* stage, int lane)
+{
+    constexpr int ES = (int)sizeof(Y), W = 128 / ES;       // columns of a 128-byte piece
+    if (rows % (16 / ES) == 0) {
+        const int r4 = lane >> 3, piece = lane & 7;
 #pragma unroll
-    for (int j = 0; j < 16; j += 4)
-        *reinterpret_cast<float4*>(stage + lane * kPad + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    __syncwarp();
+        for (int j0 = 0; j0 < C; j0 += W) {
+            const int col = c0 + (j0 >> 6) * kM + (j0 & 63) + piece * (16 / ES);
+            const bool in = col < rows;
+            if (residual) {
+                uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = i * 8 + (lane >> 2), c = (lane & 3) * 4;
-        put(i, r, c, *reinterpret_cast<const float4*>(stage + r * kPad + c));
+                for (int i = 0; i < 8; i++) {
+                    const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (to >= 0 && in) v[i] = *reinterpret_cast<const uint4*>(residual + (size_t)to * rows + col);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    *reinterpret_cast<uint4*>(stage + (i * 4 + r4) * kPitch + piece * 16) = v[i];
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 8; c++) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(stage + lane * kPitch + c * 16);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        if (ES == 4) {
+                            const int j = j0 + 4 * c + e;
+                            const float2 f = unpk2(acc[j / 2]);
+                            const float a = __uint_as_float(w[e]);
+                            acc[j / 2] = e & 1 ? pk2f(f.x, f.y + a) : pk2f(f.x + a, f.y);
+                        } else {
+                            const int j = j0 + 8 * c + 2 * e;
+                            acc[j / 2] = fadd2(acc[j / 2], pk2(w[e] << 16, w[e] & 0xFFFF0000u));
+                        }
+                    }
+                }
+            }
+            __syncwarp();        // the pieces staged before have been read
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    w[e] = ES == 4 ? __float_as_uint(acc_at(acc, j0 + 4 * c + e))
+                                   : bf16x2_bits(acc_at(acc, j0 + 8 * c + 2 * e), acc_at(acc, j0 + 8 * c + 2 * e + 1));
+                *reinterpret_cast<uint4*>(stage + lane * kPitch + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + (i * 4 + r4) * kPitch + piece * 16);
+                if (to >= 0 && in) *reinterpret_cast<uint4*>(y + (size_t)to * rows + col) = v;
+            }
+        }
+    } else {
+        // rows that do not begin on 16 bytes: 32 columns at a time, one lane a column
+        float* f = reinterpret_cast<float*>(stage);
+        constexpr int P = kPitch / 4;
+#pragma unroll
+        for (int j0 = 0; j0 < C; j0 += 32) {
+            const int col = c0 + (j0 >> 6) * kM + (j0 & 63) + lane;
+            const bool in = col < rows;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 32; j++) f[lane * P + j] = acc_at(acc, j0 + j);
+            __syncwarp();
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                float v[8];
+                size_t at[8];
+#pragma unroll
+                for (int r = 0; r < 8; r++) {
+                    const int to = __shfl_sync(0xffffffffu, orow, r0 + r);
+                    at[r] = to >= 0 && in ? (size_t)to * rows + col : ~(size_t)0;
+                    v[r] = f[(r0 + r) * P + lane] + (residual && at[r] != ~(size_t)0 ? (float)residual[at[r]] : 0.0f);
+                }
+#pragma unroll
+                for (int r = 0; r < 8; r++)
+                    if (at[r] != ~(size_t)0) y[at[r]] = (Y)v[r];
+            }
+        }
     }
-    __syncwarp();
 }
 
 template <int MODE>
@@ -184,9 +265,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the same offset in both CTAs of the pair: dynamic shared memory starts at one address in
     // every CTA of a launch
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* out_stage = reinterpret_cast<float*>(smem + kStages * (size_t)kStage);
-    uint32_t* tops = reinterpret_cast<uint32_t*>(out_stage + kOut / 4);      // [2][kM] maxima of the SwiGLU rows
-    int* first = reinterpret_cast<int*>(tops + 2 * kM);
+    uint8_t* out_stage = smem + kStages * (size_t)kStage;
+    uint32_t* tops = reinterpret_cast<uint32_t*>(out_stage + kOut);          // [2][kM] maxima of the SwiGLU rows
+    int* gtok = reinterpret_cast<int*>(tops + 2 * kM);                       // [2][kM] tokens to gather, by warp
+    int* first = gtok + 2 * kM;
     int* flags = first + (kMaxGroups + 3) / 4 * 4;         // [0] groups [1] tiles [2] last part [3] tensor memory
     uint64_t* bars = reinterpret_cast<uint64_t*>(flags + 4);
     uint64_t* full = bars;                       // [kStages] rank 0: both CTAs' tiles landed
@@ -199,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rank = (int)cluster_rank();
     if (tid == 0) {
         for (int s = 0; s < kStages; s++) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], kGather ? 1 + 2 * kGatherWarps : 1);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < kBufs; b++) {
@@ -238,38 +320,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const CUtensorMap* wm = &p.w[shared];
                 const int z = shared ? 0 : tl.g.expert;
                 const int r0 = MODE == FP8_GATE_UP ? tl.rb * kM + rank * p.I : (tl.rb * 2 + rank) * kM;
-                // token rows of each CTA; copies come in boxes or in gathered fours
-                const int n0 = min(tl.n, kM), n1 = tl.n - n0, mine = rank ? n1 : n0;
-                const int unit = kGather ? 4 : kBox;
-                const int copies = (mine + unit - 1) / unit;
-                const uint32_t bytes = 2 * kTile + (uint32_t)((n0 + unit - 1) / unit + (n1 + unit - 1) / unit) * unit * 128;
-                int4 rows = make_int4(0, 0, 0, 0);
-                if (kGather && lane < copies) {
-                    int* rr = reinterpret_cast<int*>(&rows);
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int i = tl.t0 + rank * kM + min(4 * lane + j, mine - 1);
-                        const int a = shared ? i * p.k : position_of(p, tl.g.base + i);
-                        if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                        rr[j] = max(a, 0) / p.k;
-                    }
-                }
+                // token rows of each CTA, in boxes
+                const int n0 = min(tl.n, kM), n1 = tl.n - n0;
+                const int boxes = kGather ? 0 : ((rank ? n1 : n0) + kBox - 1) / kBox;
+                const uint32_t bytes =
+                    2 * kTile + (kGather ? 0u : (uint32_t)((n0 + kBox - 1) / kBox + (n1 + kBox - 1) / kBox) * kBox * 128);
                 const int row0 = (MODE == FP8_DENSE ? tl.t0 : tl.g.base + tl.t0) + rank * kM;
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int s = n % kStages;
                     if (!dead && !mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
                     if (dead) continue;
-                    uint8_t* st = smem + (size_t)s * kStage;
-                    const uint32_t bar = map_to(&full[s], 0);
                     if (lane == 0) {
+                        uint8_t* st = smem + (size_t)s * kStage;
+                        const uint32_t bar = map_to(&full[s], 0);
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                         pair_load_3d(st + kTile, wm, kb * 128, r0, z, bar);
-                        if (!kGather)
-                            for (int b = 0; b < copies; b++)
-                                pair_load_2d(st + b * kBox * 128, &p.x, kb * 128, row0 + b * kBox, bar);
+                        for (int b = 0; b < boxes; b++)
+                            pair_load_2d(st + b * kBox * 128, &p.x, kb * 128, row0 + b * kBox, bar);
                     }
                     __syncwarp();
-                    if (kGather && lane < copies) pair_gather4(st + lane * 512, &p.x, kb * 128, rows, bar);
                 }
             }
             // no copy of the pair is in flight when it ends
@@ -305,6 +374,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 commit_pair(mma_done);
                 mbar_wait(mma_done, 0, p.status, kSite + 5);
             }
+        } else if (kGather) {
+            // ------------------- token rows by the union lists --------------------------
+            // Warp w of two copies rows 4 (2 i + w) .. + 3 of the CTA's 128 in 16-byte pieces, 8
+            // lanes a row, to where the 128-byte swizzle has them.  (Gathering tensor copies,
+            // four rows each, took 77 cycles a copy: 2500 a K step, against 700 for the MMA.)
+            const int w = warp - 10, r4 = lane >> 3, piece = lane & 7;
+            int* tok = gtok + w * kM;
+            uint32_t n = 0;
+            auto hand_over = [&](uint32_t m) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_pair(map_to(&full[m % kStages], 0));
+            };
+            while (sch.next(it)) {
+                const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
+                const int mine = min(max(tl.n - rank * kM, 0), kM);
+                __syncwarp();
+                for (int j = lane; j < mine; j += 32) {
+                    const int i = tl.t0 + rank * kM + j;
+                    const int a = tl.g.expert < 0 ? i * p.k : position_of(p, tl.g.base + i);
+                    if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
+                    tok[j] = max(a, 0) / p.k;
+                }
+                __syncwarp();
+                for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
+                    const int s = n % kStages;
+                    if (!dead && !mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 11)) dead = true;
+                    const uint32_t st = smem_u32(smem + (size_t)s * kStage);
+                    const int c = kb * 128 + piece * 16;
+                    if (!dead) {
+#pragma unroll 4
+                        for (int r = 4 * w + r4; r < mine; r += 4 * kGatherWarps)
+                            copy16(st + r * 128 + ((piece ^ (r & 7)) << 4), p.xq + (size_t)tok[r] * p.K + c, c < p.K);
+                    }
+                    cp_async_commit();
+                    if (n >= kGatherLag) {
+                        cp_async_wait<kGatherLag>();
+                        hand_over(n - kGatherLag);
+                    }
+                }
+            }
+            cp_async_wait<0>();
+            for (uint32_t m = n < kGatherLag ? 0 : n - kGatherLag; m < n; m++) hand_over(m);
         }
     } else {
         // ------------------------- scaled accumulation, outputs -------------------------
@@ -312,12 +424,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int wg = warp >> 2, q = warp & 3;     // warpgroup, tensor memory lane quarter
         const int row = q * 32 + lane;              // token within the CTA's 128
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
-        // columns of the thread: two runs of 64
-        const uint32_t ca = (uint32_t)(MODE == FP8_GATE_UP ? wg * 64 : wg * 128);
-        const uint32_t cb = (uint32_t)(MODE == FP8_GATE_UP ? 128 + wg * 64 : wg * 128 + 64);
+        // columns of the thread: 64 of each row block
+        const uint32_t ca = (uint32_t)(wg * 64), cb = ca + 128;
         uint64_t acc[C / 2];
         float* accf = reinterpret_cast<float*>(acc);
-        float* stage = out_stage + warp * 32 * kPad;
+        uint8_t* stage = out_stage + warp * 32 * kPitch;
         uint32_t n = 0;
         const uint32_t ae = map_to(&acc_empty[0], 0);
         const int nb = fp8_blocks(p.rows);
@@ -345,20 +456,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                      ? p.ws[1]
                                      : reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws[0]) +
                                                                       (uint64_t)tl.g.expert * p.ws_stride);
-            const int blk = MODE == FP8_GATE_UP ? tl.rb : min(2 * tl.rb + wg, nb - 1);
-            const float* wa = wbase + (size_t)blk * p.kb;
-            const float* wb = MODE == FP8_GATE_UP ? wa + (size_t)nb * p.kb : wa;
+            const float* wa = wbase + (size_t)(MODE == FP8_GATE_UP ? tl.rb : 2 * tl.rb) * p.kb;
+            const float* wb = MODE == FP8_GATE_UP ? wa + (size_t)nb * p.kb : 2 * tl.rb + 1 < nb ? wa + p.kb : wa;
 #pragma unroll
             for (int j = 0; j < C / 2; j++) acc[j] = 0;
             if (left > 0) {
-                float x1 = __ldg(xs + it.kb0), a1 = __ldg(wa + it.kb0), b1 = MODE == FP8_GATE_UP ? __ldg(wb + it.kb0) : 0.0f;
+                float x1 = __ldg(xs + it.kb0), a1 = __ldg(wa + it.kb0), b1 = __ldg(wb + it.kb0);
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int b = n % kBufs;
-                    const float sa = x1 * a1, sb = MODE == FP8_GATE_UP ? x1 * b1 : sa;
+                    const float sa = x1 * a1, sb = x1 * b1;
                     if (kb + 1 < it.kb1) {       // the next step's scales
                         x1 = __ldg(xs + kb + 1);
                         a1 = __ldg(wa + kb + 1);
-                        if (MODE == FP8_GATE_UP) b1 = __ldg(wb + kb + 1);
+                        b1 = __ldg(wb + kb + 1);
                     }
                     if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
                     tc_fence_after();
@@ -430,53 +540,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (MODE != FP8_GATE_UP) {
                 if (left <= 0) continue;
-                const int c0 = (2 * tl.rb + wg) * kM;            // first output column
-                const bool vec = p.rows % 4 == 0;
-#pragma unroll
-                for (int j0 = 0; j0 < C; j0 += 16) {
-                    through_smem(stage, accf + j0, lane, [&](int, int r, int c, float4 v) {
-                        const int to = __shfl_sync(0xffffffffu, orow, r);
-                        const int col = c0 + j0 + c;
-                        if (to < 0 || col >= p.rows) return;
-                        const size_t o = (size_t)to * p.rows + col;
-                        float f[4] = {v.x, v.y, v.z, v.w};
-                        if (MODE == FP8_DOWN) {
-                            *reinterpret_cast<float4*>(p.z + o) = v;
-                        } else if (p.y_bf16) {
-                            __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.y) + o;
-                            const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(p.residual) + o;
-                            if (vec) {
-                                if (p.residual) {
-                                    const uint2 u = *reinterpret_cast<const uint2*>(res);
-                                    f[0] += __uint_as_float(u.x << 16);
-                                    f[1] += __uint_as_float(u.x & 0xFFFF0000u);
-                                    f[2] += __uint_as_float(u.y << 16);
-                                    f[3] += __uint_as_float(u.y & 0xFFFF0000u);
-                                }
-                                *reinterpret_cast<uint2*>(y) = make_uint2(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]));
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 4; e++)
-                                    if (col + e < p.rows)
-                                        y[e] = __float2bfloat16_rn(f[e] + (p.residual ? __bfloat162float(res[e]) : 0.0f));
-                            }
-                        } else {
-                            float* y = reinterpret_cast<float*>(p.y) + o;
-                            const float* res = reinterpret_cast<const float*>(p.residual) + o;
-                            if (vec) {
-                                if (p.residual) {
-                                    const float4 u = *reinterpret_cast<const float4*>(res);
-                                    v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-                                }
-                                *reinterpret_cast<float4*>(y) = v;
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 4; e++)
-                                    if (col + e < p.rows) y[e] = f[e] + (p.residual ? res[e] : 0.0f);
-                            }
-                        }
-                    });
-                }
+                // output columns of the thread's two runs of 64
+                const int c0 = 2 * tl.rb * kM + wg * 64;
+                if (MODE == FP8_DOWN) store_rows<float>(p.z, nullptr, p.rows, c0, orow, acc, stage, lane);
+                else if (p.y_bf16)
+                    store_rows<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.y),
+                                              reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, orow, acc,
+                                              stage, lane);
+                else
+                    store_rows<float>(reinterpret_cast<float*>(p.y), reinterpret_cast<const float*>(p.residual), p.rows, c0,
+                                      orow, acc, stage, lane);
             } else {
                 // SwiGLU of 64 columns; the scale block is this and the other warpgroup's
                 uint32_t top = 0;

@@ -102,7 +102,7 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     Params p;
     memset(&p, 0, sizeof(p));
     const bool decode = a.T <= kDecodeTokens;
-    const int box = decode ? 16 : a.mode == FP8_GATE_UP ? 1 : 64;     // 1: rows are gathered
+    const int box = decode ? 16 : 64;     // rows of a token box
     bool ok = true;
     if (a.mode == FP8_DENSE) {
         p.K = a.K;
@@ -134,6 +134,7 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     p.E = a.E;
     p.n_shared = a.n_shared;
     p.I = a.I;
+    p.xq = a.x;
     p.xs = a.xs;
     p.union_ids = a.union_ids;
     p.n_union = a.n_union;

@@ -26,6 +26,7 @@ struct Params {
     int row_off;                  // rows before the wanted matrix inside a blob's map
     const float* ws[2];           // dense: scales; experts: first blob's scales, shared's
     uint64_t ws_stride;           // bytes between experts' scales
+    const uint8_t* xq;            // token codes and their scales
     const float* xs;
     const int32_t* union_ids;
     const int32_t* n_union;
