@@ -18,9 +18,9 @@
 // CTA, 12 warps:
 //   warps 0-7   two warpgroups: scaled accumulation, outputs
 //   warp 8      TMA producer of this CTA's weight rows and, where they lie one after another,
-//               tokens
-//   warp 9      tensor memory; in rank 0 the pair's single-thread tcgen05.mma issuer
-//   warps 10-11 GATE_UP: copies of the tokens that the union lists name
+//               tokens; GATE_UP: with warp 10, copies of the tokens that the union lists name
+//   warp 9      tensor memory; in rank 0, with warp 11, the pair's single-thread tcgen05.mma
+//               issuers, one for each warpgroup's columns
 // A part of a split tile goes to the workspace; the last one to arrive adds the parts up in
 // K order (Schedule).
 #include <string.h>
@@ -44,8 +44,8 @@ constexpr int kBox = 64;                          // rows of a token box
 constexpr int kLeast = 6;                         // K steps of a run at least
 constexpr int kPitch = 144;                       // bytes of a staged row: 128 and a gap
 constexpr size_t kOut = (size_t)kEpi * kPitch;
-constexpr int kGatherWarps = 2, kGatherLag = 3;   // warps that gather tokens, and how many K steps they run ahead
-constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 2 * kM * 4 + 2 * kM * 4 +
+constexpr int kGatherLag = 3;                     // K steps that the gathering warps run ahead
+constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 4 * kM * 4 +
                          (kMaxGroups + 3) / 4 * 4 * 4 + 16 + 256;
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -136,24 +136,13 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a));
-}
-
-// acc[16 pairs] += v[32] * s
-__device__ __forceinline__ void scaled_add(uint64_t* acc, const uint32_t (&v)[32], uint64_t s)
+// acc[8 pairs] += v[16] * s, where it stands (volatile): moved behind the next loads, all of
+// a K step's 128 values would be live at once.
+__device__ __forceinline__ void scaled_add(uint64_t* acc, const uint32_t (&v)[16], uint64_t s)
 {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) acc[j / 2] = ffma2(pk2(v[j], v[j + 1]), s, acc[j / 2]);
+    for (int j = 0; j < 16; j += 2)
+        asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[j / 2]) : "l"(pk2(v[j], v[j + 1])), "l"(s));
 }
 
 __device__ __forceinline__ float acc_at(const uint64_t (&acc)[C / 2], int j)
@@ -273,22 +262,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(flags + 4);
     uint64_t* full = bars;                       // [kStages] rank 0: both CTAs' tiles landed
     uint64_t* empty = full + kStages;            // [kStages] MMAs done with the stage
-    uint64_t* acc_full = empty + kStages;        // [kBufs] MMA commit
-    uint64_t* acc_empty = acc_full + kBufs;      // [kBufs] rank 0: read by every accumulating warp of the pair
-    uint64_t* mma_done = acc_empty + kBufs;
+    uint64_t* acc_full = empty + kStages;        // [kBufs][2] MMA commit, by warpgroup
+    uint64_t* acc_empty = acc_full + 2 * kBufs;  // [kBufs][2] rank 0: read by the warpgroup's warps in both CTAs
+    uint64_t* mma_done = acc_empty + 2 * kBufs;  // [2]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank();
     if (tid == 0) {
         for (int s = 0; s < kStages; s++) {
-            mbar_init(&full[s], kGather ? 1 + 2 * kGatherWarps : 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&full[s], kGather ? 5 : 1);
+            mbar_init(&empty[s], 2);
         }
-        for (int b = 0; b < kBufs; b++) {
+        for (int b = 0; b < 2 * kBufs; b++) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 2 * kEpi / 32);
+            mbar_init(&acc_empty[b], 2 * 4);
         }
-        mbar_init(mma_done, 1);
+        mbar_init(&mma_done[0], 1);
+        mbar_init(&mma_done[1], 1);
         fence_barrier_init();
     }
     if (warp == 9) {
@@ -310,9 +300,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Item it;
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8) {
-            // ----------------------------- TMA producer ---------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 8 || (kGather && warp == 10)) {
+            // ----------------------------- producers ------------------------------------
+            // Tokens that the union lists name: two warps copy rows 8 i + 4 w .. + 3 in 16-byte
+            // pieces, 8 lanes a row, to where the 128-byte swizzle has them.  (Gathering tensor
+            // copies, four rows each, took 77 cycles a copy: 2500 a K step, against 700 for
+            // the MMA.)
+            const int w = warp == 10, r4 = lane >> 3, piece = lane & 7;
+            int* tok = gtok + w * kM;
+            auto hand_over = [&](uint32_t m) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_pair(map_to(&full[m % kStages], 0));
+            };
             uint32_t n = 0;
             while (sch.next(it)) {
                 const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
@@ -321,17 +322,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int z = shared ? 0 : tl.g.expert;
                 const int r0 = MODE == FP8_GATE_UP ? tl.rb * kM + rank * p.I : (tl.rb * 2 + rank) * kM;
                 // token rows of each CTA, in boxes
-                const int n0 = min(tl.n, kM), n1 = tl.n - n0;
-                const int boxes = kGather ? 0 : ((rank ? n1 : n0) + kBox - 1) / kBox;
+                const int n0 = min(tl.n, kM), n1 = tl.n - n0, mine = rank ? n1 : n0;
+                const int boxes = kGather ? 0 : (mine + kBox - 1) / kBox;
                 const uint32_t bytes =
                     2 * kTile + (kGather ? 0u : (uint32_t)((n0 + kBox - 1) / kBox + (n1 + kBox - 1) / kBox) * kBox * 128);
                 const int row0 = (MODE == FP8_DENSE ? tl.t0 : tl.g.base + tl.t0) + rank * kM;
+                if (kGather) {
+                    __syncwarp();
+                    for (int j = lane; j < mine; j += 32) {
+                        const int i = tl.t0 + rank * kM + j;
+                        const int a = shared ? i * p.k : position_of(p, tl.g.base + i);
+                        if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
+                        tok[j] = max(a, 0) / p.k;
+                    }
+                    __syncwarp();
+                }
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int s = n % kStages;
                     if (!dead && !mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
-                    if (dead) continue;
-                    if (lane == 0) {
-                        uint8_t* st = smem + (size_t)s * kStage;
+                    uint8_t* st = smem + (size_t)s * kStage;
+                    if (lane == 0 && warp == 8 && !dead) {
                         const uint32_t bar = map_to(&full[s], 0);
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                         pair_load_3d(st + kTile, wm, kb * 128, r0, z, bar);
@@ -339,98 +349,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             pair_load_2d(st + b * kBox * 128, &p.x, kb * 128, row0 + b * kBox, bar);
                     }
                     __syncwarp();
+                    if (kGather) {
+                        const int c = kb * 128 + piece * 16;
+                        if (!dead) {
+#pragma unroll 4
+                            for (int r = 4 * w + r4; r < mine; r += 8)
+                                copy16(smem_u32(st) + r * 128 + ((piece ^ (r & 7)) << 4),
+                                       p.xq + (size_t)tok[r] * p.K + c, c < p.K);
+                        }
+                        cp_async_commit();
+                        if (n >= kGatherLag) {
+                            cp_async_wait<kGatherLag>();
+                            hand_over(n - kGatherLag);
+                        }
+                    }
                 }
             }
+            if (kGather) {
+                cp_async_wait<0>();
+                for (uint32_t m = n < kGatherLag ? 0 : n - kGatherLag; m < n; m++) hand_over(m);
+            }
             // no copy of the pair is in flight when it ends
-            if (lane == 0 && rank == 0) {
+            if (lane == 0 && rank == 0 && warp == 8) {
                 const uint32_t last = n < (uint32_t)kStages ? n : (uint32_t)kStages;
                 for (uint32_t i = 0; i < last; i++) {
                     const uint32_t m = n - 1 - i;
                     mbar_wait(&full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
                 }
             }
-        } else if (warp == 9) {
-            // ----------------------------- MMA issuer -----------------------------------
+        } else if (warp == 9 || warp == 11) {
+            // ----------------------------- MMA issuers -----------------------------------
+            // Each issues the MMAs of one warpgroup's columns, 64 weight rows of each CTA, into
+            // accumulator buffers of their own: a buffer is handed over and back by one
+            // warpgroup, and what the other half is up to does not hold it up.
             if (lane == 0 && rank == 0) {
-                const uint32_t idesc = idesc_e4m3(2 * kM, 2 * kM);
+                const uint32_t idesc = idesc_e4m3(2 * kM, kM), h = warp == 11;
                 uint32_t n = 0;
                 while (sch.next(it)) {
                     for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
-                        const int s = n % kStages, b = n % kBufs;
-                        if (!dead && !mbar_wait(&acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
+                        const int s = n % kStages, b = n % kBufs * 2 + h;
                         if (!dead && !mbar_wait(&full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
+                        if (!dead && !mbar_wait(&acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
                         tc_fence_after();
                         if (!dead) {
                             const uint8_t* st = smem + (size_t)s * kStage;
-                            const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + kTile);
+                            const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + kTile + h * (kTile / 2));
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)      // 32 e4m3 values = 32 bytes per MMA
-                                umma_pair(tmem + (uint32_t)(b * 256), ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
+                                umma_pair(tmem + (uint32_t)(b * 128), ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
                         }
                         commit_pair(&empty[s]);
                         commit_pair(&acc_full[b]);
                     }
                 }
-                commit_pair(mma_done);
-                mbar_wait(mma_done, 0, p.status, kSite + 5);
+                commit_pair(&mma_done[h]);
+                mbar_wait(&mma_done[h], 0, p.status, kSite + 5);
             }
-        } else if (kGather) {
-            // ------------------- token rows by the union lists --------------------------
-            // Warp w of two copies rows 4 (2 i + w) .. + 3 of the CTA's 128 in 16-byte pieces, 8
-            // lanes a row, to where the 128-byte swizzle has them.  (Gathering tensor copies,
-            // four rows each, took 77 cycles a copy: 2500 a K step, against 700 for the MMA.)
-            const int w = warp - 10, r4 = lane >> 3, piece = lane & 7;
-            int* tok = gtok + w * kM;
-            uint32_t n = 0;
-            auto hand_over = [&](uint32_t m) {
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_pair(map_to(&full[m % kStages], 0));
-            };
-            while (sch.next(it)) {
-                const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
-                const int mine = min(max(tl.n - rank * kM, 0), kM);
-                __syncwarp();
-                for (int j = lane; j < mine; j += 32) {
-                    const int i = tl.t0 + rank * kM + j;
-                    const int a = tl.g.expert < 0 ? i * p.k : position_of(p, tl.g.base + i);
-                    if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                    tok[j] = max(a, 0) / p.k;
-                }
-                __syncwarp();
-                for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
-                    const int s = n % kStages;
-                    if (!dead && !mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 11)) dead = true;
-                    const uint32_t st = smem_u32(smem + (size_t)s * kStage);
-                    const int c = kb * 128 + piece * 16;
-                    if (!dead) {
-#pragma unroll 4
-                        for (int r = 4 * w + r4; r < mine; r += 4 * kGatherWarps)
-                            copy16(st + r * 128 + ((piece ^ (r & 7)) << 4), p.xq + (size_t)tok[r] * p.K + c, c < p.K);
-                    }
-                    cp_async_commit();
-                    if (n >= kGatherLag) {
-                        cp_async_wait<kGatherLag>();
-                        hand_over(n - kGatherLag);
-                    }
-                }
-            }
-            cp_async_wait<0>();
-            for (uint32_t m = n < kGatherLag ? 0 : n - kGatherLag; m < n; m++) hand_over(m);
         }
     } else {
         // ------------------------- scaled accumulation, outputs -------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int wg = warp >> 2, q = warp & 3;     // warpgroup, tensor memory lane quarter
         const int row = q * 32 + lane;              // token within the CTA's 128
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
-        // columns of the thread: 64 of each row block
-        const uint32_t ca = (uint32_t)(wg * 64), cb = ca + 128;
         uint64_t acc[C / 2];
         float* accf = reinterpret_cast<float*>(acc);
         uint8_t* stage = out_stage + warp * 32 * kPitch;
         uint32_t n = 0;
-        const uint32_t ae = map_to(&acc_empty[0], 0);
+        const uint32_t ae = map_to(&acc_empty[wg], 0);
         const int nb = fp8_blocks(p.rows);
         while (sch.next(it)) {
             const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
@@ -461,43 +447,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < C / 2; j++) acc[j] = 0;
             if (left > 0) {
-                float x1 = __ldg(xs + it.kb0), a1 = __ldg(wa + it.kb0), b1 = __ldg(wb + it.kb0);
-                for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
-                    const int b = n % kBufs;
-                    const float sa = x1 * a1, sb = x1 * b1;
-                    if (kb + 1 < it.kb1) {       // the next step's scales
-                        x1 = __ldg(xs + kb + 1);
-                        a1 = __ldg(wa + kb + 1);
-                        b1 = __ldg(wb + kb + 1);
+                // scales of four K steps at a time, fetched four steps ahead
+                float xn[4], an[4], bn[4];
+                auto fetch = [&](int kb) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int k = min(kb + i, it.kb1 - 1);
+                        xn[i] = __ldg(xs + k);
+                        an[i] = __ldg(wa + k);
+                        bn[i] = __ldg(wb + k);
                     }
-                    if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
-                    tc_fence_after();
-                    const uint32_t ta = lane_addr + (uint32_t)(b * 256);
-                    // loads run one chunk of 32 columns ahead of the arithmetic
-                    uint32_t v0[32], v1[32];
-                    tmem_ld32(ta + ca, v0);
-                    tmem_wait_ld();
-                    tmem_ld32(ta + ca + 32, v1);
-                    scaled_add(acc, v0, pk2f(sa, sa));
-                    tmem_wait_ld();
-                    tmem_ld32(ta + cb, v0);
-                    scaled_add(acc + 16, v1, pk2f(sa, sa));
-                    tmem_wait_ld();
-                    tmem_ld32(ta + cb + 32, v1);
-                    scaled_add(acc + 32, v0, pk2f(sb, sb));
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_pair(ae + b * 8);
-                    scaled_add(acc + 48, v1, pk2f(sb, sb));
+                };
+                fetch(it.kb0);
+                for (int kb = it.kb0; kb < it.kb1; kb += 4) {
+                    float sa[4], sb[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        sa[i] = xn[i] * an[i];
+                        sb[i] = xn[i] * bn[i];
+                    }
+                    if (kb + 4 < it.kb1) fetch(kb + 4);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        if (kb + i >= it.kb1) break;
+                        const int b = n % kBufs;
+                        if (!dead && !mbar_wait(&acc_full[2 * b + wg], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                        tc_fence_after();
+                        const uint32_t ta = lane_addr + (uint32_t)(b * 256 + wg * 128);
+                        // loads run one chunk of 16 columns ahead of the arithmetic
+                        uint32_t v[2][16];
+                        tmem_ld16(ta, v[0]);
+#pragma unroll
+                        for (int c = 0; c < 8; c++) {
+                            tmem_wait_ld();
+                            if (c < 7) tmem_ld16(ta + (c + 1) * 16, v[(c + 1) & 1]);
+                            else {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) arrive_pair(ae + b * 16);
+                            }
+                            scaled_add(acc + c * 8, v[c & 1], c < 4 ? pk2f(sa[i], sa[i]) : pk2f(sb[i], sb[i]));
+                        }
+                        n++;
+                    }
                 }
             } else {
                 // no token in this warp: only hand the buffers on
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int b = n % kBufs;
-                    if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                    if (!dead && !mbar_wait(&acc_full[2 * b + wg], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
                     __syncwarp();
-                    if (lane == 0) arrive_pair(ae + b * 8);
+                    if (lane == 0) arrive_pair(ae + b * 16);
                 }
             }
             if (it.kb1 - it.kb0 < p.kb) {
