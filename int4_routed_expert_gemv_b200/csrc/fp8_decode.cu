@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                     mbar_arrive_expect_tx(&full[s], kStage);
                     tma_load_3d(st, wm, kb * 128, r0, z, &full[s]);
                     tma_load_3d(st + kM * 128, wm, kb * 128, r1, z, &full[s]);
-                    tma_load_2d(st + 2 * kM * 128, &p.x, kb * 128, row0, &full[s]);
+                    tma_load_2d(st + 2 * kM * 128, &p.x[0], kb * 128, row0, &full[s]);
                 }
             }
         }

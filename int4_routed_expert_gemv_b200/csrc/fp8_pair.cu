@@ -11,16 +11,20 @@
 // weights there, the scales of all columns come from shared memory, and those reads, beside
 // the MMA's own, took 3 times as long as everything else.
 //
+// The tokens of an expert lie one after another: GATE_UP reads a copy in list order, made by
+// a launch before.  (Gathering tensor copies, four rows each, took 77 cycles a copy, 2500 a
+// K step; cp.async by two warps 2000, as each hand-over to the MMA waits for the copies
+// behind it.)
+//
 // The two row blocks of a tile: DENSE and DOWN neighbours, GATE_UP the gate and the up rows of
 // the same 128 intermediate columns, which are one scale block of h.  Warpgroup g has columns
 // 64 g .. of both.
 //
 // CTA, 12 warps:
 //   warps 0-7   two warpgroups: scaled accumulation, outputs
-//   warp 8      TMA producer of this CTA's weight rows and, where they lie one after another,
-//               tokens; GATE_UP: with warp 10, copies of the tokens that the union lists name
+//   warp 8      TMA producer of this CTA's tokens and weight rows
 //   warp 9      tensor memory; in rank 0, with warp 11, the pair's single-thread tcgen05.mma
-//               issuers, one for each warpgroup's columns
+//               issuers, a K step each in turn
 // A part of a split tile goes to the workspace; the last one to arrive adds the parts up in
 // K order (Schedule).
 #include <string.h>
@@ -44,8 +48,7 @@ constexpr int kBox = 64;                          // rows of a token box
 constexpr int kLeast = 6;                         // K steps of a run at least
 constexpr int kPitch = 144;                       // bytes of a staged row: 128 and a gap
 constexpr size_t kOut = (size_t)kEpi * kPitch;
-constexpr int kGatherLag = 3;                     // K steps that the gathering warps run ahead
-constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 4 * kM * 4 +
+constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 2 * kM * 4 +
                          (kMaxGroups + 3) / 4 * 4 * 4 + 16 + 256;
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -109,12 +112,6 @@ __device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, 
         : "memory");
 }
 
-// 16 bytes global -> shared, zeros where `in` is false.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-
 __device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate)
 {
@@ -136,19 +133,12 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar)
         : "memory");
 }
 
-// acc[8 pairs] += v[16] * s, where it stands (volatile): moved behind the next loads, all of
-// a K step's 128 values would be live at once.
-__device__ __forceinline__ void scaled_add(uint64_t* acc, const uint32_t (&v)[16], uint64_t s)
+// acc[16] += v[16] * s.  Single FFMAs: packed pairs cost more in moves, since the values that
+// tcgen05.ld leaves are not where pairs have to be.
+__device__ __forceinline__ void scaled_add(float* acc, const uint32_t (&v)[16], float s)
 {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2)
-        asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[j / 2]) : "l"(pk2(v[j], v[j + 1])), "l"(s));
-}
-
-__device__ __forceinline__ float acc_at(const uint64_t (&acc)[C / 2], int j)
-{
-    const float2 f = unpk2(acc[j / 2]);
-    return j & 1 ? f.y : f.x;
+    for (int j = 0; j < 16; j++) acc[j] = fmaf(__uint_as_float(v[j]), s, acc[j]);
 }
 
 // A warp's 32 rows of outputs, one per thread (orow: its row of y, -1 for none): two runs of 64
@@ -156,7 +146,7 @@ __device__ __forceinline__ float acc_at(const uint64_t (&acc)[C / 2], int j)
 // memory, 128 bytes each at a time, so that 8 neighbouring lanes write (and read the
 // residual's) 128 consecutive bytes; the loads of a piece are under way together.
 template <class Y>
-__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, uint64_t (&acc)[C / 2],
+__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, float (&acc)[C],
                                            uint8_t* stage, int lane)
 {
     constexpr int ES = (int)sizeof(Y), W = 128 / ES;       // columns of a 128-byte piece
@@ -186,13 +176,10 @@ __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, in
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         if (ES == 4) {
-                            const int j = j0 + 4 * c + e;
-                            const float2 f = unpk2(acc[j / 2]);
-                            const float a = __uint_as_float(w[e]);
-                            acc[j / 2] = e & 1 ? pk2f(f.x, f.y + a) : pk2f(f.x + a, f.y);
+                            acc[j0 + 4 * c + e] += __uint_as_float(w[e]);
                         } else {
-                            const int j = j0 + 8 * c + 2 * e;
-                            acc[j / 2] = fadd2(acc[j / 2], pk2(w[e] << 16, w[e] & 0xFFFF0000u));
+                            acc[j0 + 8 * c + 2 * e] += __uint_as_float(w[e] << 16);
+                            acc[j0 + 8 * c + 2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
                         }
                     }
                 }
@@ -203,8 +190,8 @@ __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, in
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    w[e] = ES == 4 ? __float_as_uint(acc_at(acc, j0 + 4 * c + e))
-                                   : bf16x2_bits(acc_at(acc, j0 + 8 * c + 2 * e), acc_at(acc, j0 + 8 * c + 2 * e + 1));
+                    w[e] = ES == 4 ? __float_as_uint(acc[j0 + 4 * c + e])
+                                   : bf16x2_bits(acc[j0 + 8 * c + 2 * e], acc[j0 + 8 * c + 2 * e + 1]);
                 *reinterpret_cast<uint4*>(stage + lane * kPitch + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             __syncwarp();
@@ -225,7 +212,7 @@ __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, in
             const bool in = col < rows;
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; j++) f[lane * P + j] = acc_at(acc, j0 + j);
+            for (int j = 0; j < 32; j++) f[lane * P + j] = acc[j0 + j];
             __syncwarp();
             for (int r0 = 0; r0 < 32; r0 += 8) {
                 float v[8];
@@ -248,34 +235,31 @@ template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ Params p)
 {
-    constexpr bool kGather = MODE == FP8_GATE_UP;
-
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // the same offset in both CTAs of the pair: dynamic shared memory starts at one address in
     // every CTA of a launch
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* out_stage = smem + kStages * (size_t)kStage;
     uint32_t* tops = reinterpret_cast<uint32_t*>(out_stage + kOut);          // [2][kM] maxima of the SwiGLU rows
-    int* gtok = reinterpret_cast<int*>(tops + 2 * kM);                       // [2][kM] tokens to gather, by warp
-    int* first = gtok + 2 * kM;
+    int* first = reinterpret_cast<int*>(tops + 2 * kM);
     int* flags = first + (kMaxGroups + 3) / 4 * 4;         // [0] groups [1] tiles [2] last part [3] tensor memory
     uint64_t* bars = reinterpret_cast<uint64_t*>(flags + 4);
     uint64_t* full = bars;                       // [kStages] rank 0: both CTAs' tiles landed
     uint64_t* empty = full + kStages;            // [kStages] MMAs done with the stage
-    uint64_t* acc_full = empty + kStages;        // [kBufs][2] MMA commit, by warpgroup
-    uint64_t* acc_empty = acc_full + 2 * kBufs;  // [kBufs][2] rank 0: read by the warpgroup's warps in both CTAs
-    uint64_t* mma_done = acc_empty + 2 * kBufs;  // [2]
+    uint64_t* acc_full = empty + kStages;        // [kBufs] MMA commit
+    uint64_t* acc_empty = acc_full + kBufs;      // [kBufs] rank 0: read by every accumulating warp of the pair
+    uint64_t* mma_done = acc_empty + kBufs;      // [2]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank();
     if (tid == 0) {
         for (int s = 0; s < kStages; s++) {
-            mbar_init(&full[s], kGather ? 5 : 1);
-            mbar_init(&empty[s], 2);
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2 * kBufs; b++) {
+        for (int b = 0; b < kBufs; b++) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 2 * 4);
+            mbar_init(&acc_empty[b], 2 * kEpi / 32);
         }
         mbar_init(&mma_done[0], 1);
         mbar_init(&mma_done[1], 1);
@@ -301,76 +285,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 8 || (kGather && warp == 10)) {
-            // ----------------------------- producers ------------------------------------
-            // Tokens that the union lists name: two warps copy rows 8 i + 4 w .. + 3 in 16-byte
-            // pieces, 8 lanes a row, to where the 128-byte swizzle has them.  (Gathering tensor
-            // copies, four rows each, took 77 cycles a copy: 2500 a K step, against 700 for
-            // the MMA.)
-            const int w = warp == 10, r4 = lane >> 3, piece = lane & 7;
-            int* tok = gtok + w * kM;
-            auto hand_over = [&](uint32_t m) {
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_pair(map_to(&full[m % kStages], 0));
-            };
+        if (warp == 8) {
+            // ----------------------------- TMA producer ---------------------------------
             uint32_t n = 0;
             while (sch.next(it)) {
                 const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
                 const int shared = tl.g.expert < 0 ? 1 : 0;
                 const CUtensorMap* wm = &p.w[shared];
+                const CUtensorMap* xm = &p.x[MODE == FP8_GATE_UP ? shared : 0];
                 const int z = shared ? 0 : tl.g.expert;
                 const int r0 = MODE == FP8_GATE_UP ? tl.rb * kM + rank * p.I : (tl.rb * 2 + rank) * kM;
                 // token rows of each CTA, in boxes
-                const int n0 = min(tl.n, kM), n1 = tl.n - n0, mine = rank ? n1 : n0;
-                const int boxes = kGather ? 0 : (mine + kBox - 1) / kBox;
-                const uint32_t bytes =
-                    2 * kTile + (kGather ? 0u : (uint32_t)((n0 + kBox - 1) / kBox + (n1 + kBox - 1) / kBox) * kBox * 128);
-                const int row0 = (MODE == FP8_DENSE ? tl.t0 : tl.g.base + tl.t0) + rank * kM;
-                if (kGather) {
-                    __syncwarp();
-                    for (int j = lane; j < mine; j += 32) {
-                        const int i = tl.t0 + rank * kM + j;
-                        const int a = shared ? i * p.k : position_of(p, tl.g.base + i);
-                        if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                        tok[j] = max(a, 0) / p.k;
-                    }
-                    __syncwarp();
-                }
+                const int n0 = min(tl.n, kM), n1 = tl.n - n0;
+                const int boxes = ((rank ? n1 : n0) + kBox - 1) / kBox;
+                const uint32_t bytes = 2 * kTile + (uint32_t)((n0 + kBox - 1) / kBox + (n1 + kBox - 1) / kBox) * kBox * 128;
+                const int base = MODE == FP8_DENSE || (MODE == FP8_GATE_UP && shared) ? 0 : tl.g.base;
+                const int row0 = base + tl.t0 + rank * kM;
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int s = n % kStages;
                     if (!dead && !mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
-                    uint8_t* st = smem + (size_t)s * kStage;
-                    if (lane == 0 && warp == 8 && !dead) {
+                    if (dead) continue;
+                    if (lane == 0) {
+                        uint8_t* st = smem + (size_t)s * kStage;
                         const uint32_t bar = map_to(&full[s], 0);
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                         pair_load_3d(st + kTile, wm, kb * 128, r0, z, bar);
                         for (int b = 0; b < boxes; b++)
-                            pair_load_2d(st + b * kBox * 128, &p.x, kb * 128, row0 + b * kBox, bar);
+                            pair_load_2d(st + b * kBox * 128, xm, kb * 128, row0 + b * kBox, bar);
                     }
                     __syncwarp();
-                    if (kGather) {
-                        const int c = kb * 128 + piece * 16;
-                        if (!dead) {
-#pragma unroll 4
-                            for (int r = 4 * w + r4; r < mine; r += 8)
-                                copy16(smem_u32(st) + r * 128 + ((piece ^ (r & 7)) << 4),
-                                       p.xq + (size_t)tok[r] * p.K + c, c < p.K);
-                        }
-                        cp_async_commit();
-                        if (n >= kGatherLag) {
-                            cp_async_wait<kGatherLag>();
-                            hand_over(n - kGatherLag);
-                        }
-                    }
                 }
             }
-            if (kGather) {
-                cp_async_wait<0>();
-                for (uint32_t m = n < kGatherLag ? 0 : n - kGatherLag; m < n; m++) hand_over(m);
-            }
             // no copy of the pair is in flight when it ends
-            if (lane == 0 && rank == 0 && warp == 8) {
+            if (lane == 0 && rank == 0) {
                 const uint32_t last = n < (uint32_t)kStages ? n : (uint32_t)kStages;
                 for (uint32_t i = 0; i < last; i++) {
                     const uint32_t m = n - 1 - i;
@@ -379,31 +326,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 9 || warp == 11) {
             // ----------------------------- MMA issuers -----------------------------------
-            // Each issues the MMAs of one warpgroup's columns, 64 weight rows of each CTA, into
-            // accumulator buffers of their own: a buffer is handed over and back by one
-            // warpgroup, and what the other half is up to does not hold it up.
+            // K steps alternate between the two: an issuer is held up until its MMAs have nearly
+            // run, and the other waits for the next step's barriers meanwhile.  (256 columns an
+            // MMA: two of 128, with buffers of their own, took as long each.)
             if (lane == 0 && rank == 0) {
-                const uint32_t idesc = idesc_e4m3(2 * kM, kM), h = warp == 11;
+                const uint32_t idesc = idesc_e4m3(2 * kM, 2 * kM), odd = warp == 11;
                 uint32_t n = 0;
                 while (sch.next(it)) {
                     for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
-                        const int s = n % kStages, b = n % kBufs * 2 + h;
+                        if ((n & 1) != odd) continue;
+                        const int s = n % kStages, b = n % kBufs;
+                        const uint8_t* st = smem + (size_t)s * kStage;
+                        const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + kTile);
                         if (!dead && !mbar_wait(&full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
                         if (!dead && !mbar_wait(&acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
                         tc_fence_after();
                         if (!dead) {
-                            const uint8_t* st = smem + (size_t)s * kStage;
-                            const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + kTile + h * (kTile / 2));
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)      // 32 e4m3 values = 32 bytes per MMA
-                                umma_pair(tmem + (uint32_t)(b * 128), ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
+                                umma_pair(tmem + (uint32_t)(b * 256), ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
                         }
-                        commit_pair(&empty[s]);
                         commit_pair(&acc_full[b]);
+                        commit_pair(&empty[s]);
                     }
                 }
-                commit_pair(&mma_done[h]);
-                mbar_wait(&mma_done[h], 0, p.status, kSite + 5);
+                commit_pair(&mma_done[odd]);
+                mbar_wait(&mma_done[odd], 0, p.status, kSite + 5);
             }
         }
     } else {
@@ -412,11 +360,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int wg = warp >> 2, q = warp & 3;     // warpgroup, tensor memory lane quarter
         const int row = q * 32 + lane;              // token within the CTA's 128
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
-        uint64_t acc[C / 2];
-        float* accf = reinterpret_cast<float*>(acc);
+        float acc[C];
         uint8_t* stage = out_stage + warp * 32 * kPitch;
         uint32_t n = 0;
-        const uint32_t ae = map_to(&acc_empty[wg], 0);
+        const uint32_t ae = map_to(&acc_empty[0], 0);
         const int nb = fp8_blocks(p.rows);
         while (sch.next(it)) {
             const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
@@ -434,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     else if (tl.g.expert >= 0 && tl.rb == 0 && wg == 0) p.present[a] = 1;
                 } else {
                     if (tl.g.expert >= 0) xrow = max(a, 0) / p.k;
-                    orow = tl.g.base + tok;
+                    orow = a < 0 ? -1 : tl.g.base + tok;
                 }
             }
             const float* xs = p.xs + (size_t)(valid ? xrow : 0) * p.kb;
@@ -445,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float* wa = wbase + (size_t)(MODE == FP8_GATE_UP ? tl.rb : 2 * tl.rb) * p.kb;
             const float* wb = MODE == FP8_GATE_UP ? wa + (size_t)nb * p.kb : 2 * tl.rb + 1 < nb ? wa + p.kb : wa;
 #pragma unroll
-            for (int j = 0; j < C / 2; j++) acc[j] = 0;
+            for (int j = 0; j < C; j++) acc[j] = 0.0f;
             if (left > 0) {
                 // scales of four K steps at a time, fetched four steps ahead
                 float xn[4], an[4], bn[4];
@@ -471,22 +418,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; i++) {
                         if (kb + i >= it.kb1) break;
                         const int b = n % kBufs;
-                        if (!dead && !mbar_wait(&acc_full[2 * b + wg], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                        if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
                         tc_fence_after();
-                        const uint32_t ta = lane_addr + (uint32_t)(b * 256 + wg * 128);
+                        const uint32_t ta = lane_addr + (uint32_t)(b * 256 + wg * 64);
                         // loads run one chunk of 16 columns ahead of the arithmetic
                         uint32_t v[2][16];
                         tmem_ld16(ta, v[0]);
 #pragma unroll
                         for (int c = 0; c < 8; c++) {
                             tmem_wait_ld();
-                            if (c < 7) tmem_ld16(ta + (c + 1) * 16, v[(c + 1) & 1]);
+                            if (c < 7) tmem_ld16(ta + (c + 1) * 16 + (c >= 3 ? 64 : 0), v[(c + 1) & 1]);
                             else {
                                 tc_fence_before();
                                 __syncwarp();
-                                if (lane == 0) arrive_pair(ae + b * 16);
+                                if (lane == 0) arrive_pair(ae + b * 8);
                             }
-                            scaled_add(acc + c * 8, v[c & 1], c < 4 ? pk2f(sa[i], sa[i]) : pk2f(sb[i], sb[i]));
+                            scaled_add(acc + c * 16, v[c & 1], c < 4 ? sa[i] : sb[i]);
                         }
                         n++;
                     }
@@ -495,9 +442,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // no token in this warp: only hand the buffers on
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int b = n % kBufs;
-                    if (!dead && !mbar_wait(&acc_full[2 * b + wg], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                    if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
                     __syncwarp();
-                    if (lane == 0) arrive_pair(ae + b * 16);
+                    if (lane == 0) arrive_pair(ae + b * 8);
                 }
             }
             if (it.kb1 - it.kb0 < p.kb) {
@@ -508,8 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (left > 0) {
 #pragma unroll
                     for (int j = 0; j < C / 4; j++) {
-                        const float2 a = unpk2(acc[2 * j]), b2 = unpk2(acc[2 * j + 1]);
-                        __stcg(dst + j * kEpi, make_float4(a.x, a.y, b2.x, b2.y));
+                        __stcg(dst + j * kEpi, make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
                     }
                 }
                 __threadfence();
@@ -525,15 +471,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __threadfence();
                 if (left > 0) {
 #pragma unroll
-                    for (int j = 0; j < C / 2; j++) acc[j] = 0;
+                    for (int j = 0; j < C; j++) acc[j] = 0.0f;
                     for (int o = o0; o <= o1; o++) {
                         const float4* src = reinterpret_cast<const float4*>(p.partial) +
                                             ((size_t)(2 * o + (o == o0 ? 1 : 0)) * 2 + rank) * (C / 4) * kEpi + tid;
 #pragma unroll
                         for (int j = 0; j < C / 4; j++) {
                             const float4 f = __ldcg(src + (size_t)j * kEpi);
-                            acc[2 * j] = fadd2(acc[2 * j], pk2f(f.x, f.y));
-                            acc[2 * j + 1] = fadd2(acc[2 * j + 1], pk2f(f.z, f.w));
+                            acc[4 * j] += f.x;
+                            acc[4 * j + 1] += f.y;
+                            acc[4 * j + 2] += f.z;
+                            acc[4 * j + 3] += f.w;
                         }
                     }
                 }
@@ -556,8 +504,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (left > 0 && tl.rb * kM + wg * 64 < p.I) {            // I is a multiple of 64
 #pragma unroll
                     for (int j = 0; j < 64; j++) {
-                        accf[j] = swiglu(accf[j], accf[64 + j]);
-                        top = max(top, __float_as_uint(accf[j]) & 0x7FFFFFFFu);
+                        acc[j] = swiglu(acc[j], acc[64 + j]);
+                        top = max(top, __float_as_uint(acc[j]) & 0x7FFFFFFFu);
                     }
                 }
                 tops[wg * kM + row] = top;
@@ -573,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
-                            const float* f = accf + j + 4 * e;
+                            const float* f = acc + j + 4 * e;
                             w[e] = (uint32_t)code_of(f[0], scale) | (uint32_t)code_of(f[1], scale) << 8 |
                                    (uint32_t)code_of(f[2], scale) << 16 | (uint32_t)code_of(f[3], scale) << 24;
                         }

@@ -49,6 +49,22 @@ __global__ void __launch_bounds__(256) fp8_combine_kernel(int T, int k, int H, i
     }
 }
 
+// Rows of x in list order: row p is token assign[p] / k.  Positions that are none of the
+// batch's are flagged and leave their row as it is.
+__global__ void __launch_bounds__(256) fp8_gather_kernel(int positions, int k, int E, int pieces, const int32_t* n_union,
+                                                         const int32_t* offsets, const int32_t* assign, const uint4* x,
+                                                         uint4* to, uint32_t* status)
+{
+    const int nu = min(max(*n_union, 0), E);
+    const int64_t total = (int64_t)min(max(offsets[nu], 0), positions) * pieces;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int p = (int)(i / pieces), c = (int)(i - (int64_t)p * pieces);
+        const int a = assign[p];
+        if (a >= 0 && a < positions) to[i] = __ldg(x + (size_t)(a / k) * pieces + c);
+        else set_flag(status, DEV_BAD_INDEX);
+    }
+}
+
 // ------------------------------------------------------------------------------------
 // host side
 // ------------------------------------------------------------------------------------
@@ -93,6 +109,7 @@ inline size_t partial_bytes(int64_t T)
 size_t fp8_scratch_bytes(int mode, int64_t T, int H, int k, int n_shared)
 {
     size_t n = partial_bytes(T);
+    if (mode == FP8_GATE_UP && T > kDecodeTokens) n += up((size_t)T * k * H);
     if (mode == FP8_DOWN) n += up((size_t)T * k) + up((size_t)T * (k + n_shared) * H * sizeof(float));
     return n;
 }
@@ -103,13 +120,14 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     memset(&p, 0, sizeof(p));
     const bool decode = a.T <= kDecodeTokens;
     const int box = decode ? 16 : 64;     // rows of a token box
+    uint8_t* gathered = a.scratch + partial_bytes(a.T);
     bool ok = true;
     if (a.mode == FP8_DENSE) {
         p.K = a.K;
         p.rows = a.N;
         ok &= weight_map(&p.w[0], a.w, a.K, a.N, 1, (uint64_t)a.K * a.N);
         p.ws[0] = a.wscale;
-        ok &= token_map(&p.x, a.x, a.K, a.T, box);
+        ok &= token_map(&p.x[0], a.x, a.K, a.T, box);
     } else {
         const bool gu = a.mode == FP8_GATE_UP;
         const uint64_t IH = (uint64_t)a.I * a.H;
@@ -124,7 +142,12 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
         p.ws[0] = reinterpret_cast<const float*>(a.experts + sc);
         p.ws[1] = reinterpret_cast<const float*>(sh + sc);
         p.ws_stride = a.stride;
-        ok &= token_map(&p.x, a.x, p.K, gu ? a.T : (uint64_t)a.T * (a.k + a.n_shared), box);
+        if (gu && !decode) {
+            ok &= token_map(&p.x[0], gathered, p.K, (uint64_t)a.T * a.k, box);
+            ok &= token_map(&p.x[1], a.x, p.K, a.T, box);
+        } else {
+            ok &= token_map(&p.x[0], a.x, p.K, gu ? a.T : (uint64_t)a.T * (a.k + a.n_shared), box);
+        }
     }
     if (!ok) return cudaErrorInvalidValue;
     p.kb = fp8_blocks(p.K);
@@ -134,7 +157,6 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     p.E = a.E;
     p.n_shared = a.n_shared;
     p.I = a.I;
-    p.xq = a.x;
     p.xs = a.xs;
     p.union_ids = a.union_ids;
     p.n_union = a.n_union;
@@ -151,6 +173,15 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     auto product = [&]() {
         return decode ? fp8_decode_launch(a.mode, p, a.num_sms, s) : fp8_pair_launch(a.mode, p, a.num_sms, s);
     };
+    if (a.mode == FP8_GATE_UP && !decode) {
+        const int64_t pieces = (int64_t)a.T * a.k * (a.H / 16);
+        const int blocks = (int)(pieces + 255 < (int64_t)256 * a.num_sms * 8 ? (pieces + 255) / 256 : (int64_t)a.num_sms * 8);
+        fp8_gather_kernel<<<blocks, 256, 0, s>>>(a.T * a.k, a.k, a.E, a.H / 16, a.n_union, a.offsets, a.assign,
+                                                 reinterpret_cast<const uint4*>(a.x), reinterpret_cast<uint4*>(gathered),
+                                                 a.status);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     if (a.mode != FP8_DOWN) return product();
     uint8_t* at = a.scratch + partial_bytes(a.T);
     p.present = at;

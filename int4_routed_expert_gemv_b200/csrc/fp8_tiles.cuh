@@ -19,15 +19,14 @@ constexpr int kMaxGroups = 1024 + 1;    // experts and the shared one
 // Parameters of a launch.
 struct Params {
     CUtensorMap w[2];             // dense or routed experts, shared expert
-    CUtensorMap x;
+    CUtensorMap x[2];             // tokens; GATE_UP above 16 tokens: in list order, and as given
     int K, kb;                    // contraction length and its scale blocks
     int rows, rb;                 // output rows of a matrix, 256-row (or gate/up pair) blocks
     int T, k, E, n_shared, I;
     int row_off;                  // rows before the wanted matrix inside a blob's map
     const float* ws[2];           // dense: scales; experts: first blob's scales, shared's
     uint64_t ws_stride;           // bytes between experts' scales
-    const uint8_t* xq;            // token codes and their scales
-    const float* xs;
+    const float* xs;              // scales of the token codes
     const int32_t* union_ids;
     const int32_t* n_union;
     const int32_t* offsets;
