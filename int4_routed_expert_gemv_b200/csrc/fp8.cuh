@@ -4,6 +4,7 @@
 // Scales: an activation row has one per 128 columns ([rows][ceil(cols / 128)]), a weight
 // matrix one per 128 rows and 128 columns ([ceil(rows / 128)][ceil(cols / 128)]).
 #pragma once
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -15,6 +16,39 @@ constexpr float kFp8Max = 448.0f;     // largest e4m3 value
 constexpr int kFp8Ctas = 148;         // CTAs of a product launch at most (one per SM)
 
 __host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+#ifdef __CUDACC__
+// Codes of one scale block: scale = max / 448, code = e4m3(v / scale), 0 at scale 0.  The fp32
+// quotient is formed as P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor" (1990), does: a correctly rounded reciprocal, the product, its exact
+// remainder and one correction give the correctly rounded quotient, as long as nothing
+// underflows.  The remainder's last bit is 2^-48 of v, so with a scale of 2^-90 or more every v
+// that is not far below the smallest code is safe; other scales take the division.
+struct Quantizer {
+    float scale, r;
+    bool plain;      // by division
+
+    // max_bits: bits of the largest |v| (a NaN's are above every number's)
+    __device__ __forceinline__ explicit Quantizer(uint32_t max_bits)
+    {
+        scale = __fdiv_rn(__uint_as_float(max_bits), kFp8Max);
+        r = __frcp_rn(scale);
+        plain = !(scale >= 0x1p-90f && scale <= 0x1p90f);
+    }
+    __device__ __forceinline__ float quotient(float v) const
+    {
+        const float q = __fmul_rn(v, r);
+        return __fmaf_rn(__fmaf_rn(-q, scale, v), r, q);
+    }
+    // codes of a (low byte) and b
+    __device__ __forceinline__ uint32_t codes(float a, float b) const
+    {
+        float2 v = make_float2(quotient(a), quotient(b));
+        if (plain) v = scale == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
+        return (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    }
+};
+#endif
 
 // Bytes of one expert blob: Gq | Uq | Dq (one byte per weight) | Gs | Us | Ds (fp32).
 inline size_t fp8_blob_bytes(int H, int I)

@@ -322,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                     if (j >= mine) break;
                     const uint32_t* t4 = tops + wg * 4 * C + j;
                     const uint32_t t = max(max(t4[0], t4[C]), max(t4[2 * C], t4[3 * C]));
-                    const float scale = __fdiv_rn(__uint_as_float(t), kFp8Max);
+                    const Quantizer qz(t);
                     const int pos = cp[j];
                     if (pos < 0 || i >= p.I) continue;
-                    p.hq[(size_t)pos * p.I + i] = code_of(accf[j], scale);
-                    if (row == 0) p.hs[(size_t)pos * ib + tl.rb] = scale;
+                    p.hq[(size_t)pos * p.I + i] = (uint8_t)qz.codes(accf[j], 0.0f);
+                    if (row == 0) p.hs[(size_t)pos * ib + tl.rb] = qz.scale;
                 }
                 named_bar(2 + wg, 128);      // the maxima are read before the next tile's
             }

@@ -12,7 +12,6 @@
 // reduced across the CTA, and written out as sum, n, codes and scales.  16 neighbouring lanes
 // hold one scale block, so its maximum is four shuffles.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "common.cuh"
 #include "fp8.cuh"
@@ -139,22 +138,15 @@ __global__ void __launch_bounds__(STEPS == 4 ? 1024 : 768) fp8_norm_kernel(Fp8No
         for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (!in) continue;
         if (p.out) store8<false>(p.out, row + c, r[i]);
-        const float scale = __fdiv_rn(__uint_as_float(top), kFp8Max);
+        const Quantizer qz(top);
         uint32_t w[2];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            uint32_t b = 0;
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                float2 v = make_float2(0.0f, 0.0f);
-                if (scale != 0.0f)
-                    v = make_float2(__fdiv_rn(r[i].v[4 * h + j], scale), __fdiv_rn(r[i].v[4 * h + j + 1], scale));
-                b |= (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3) << (8 * j);
-            }
-            w[h] = b;
+            const float* f = r[i].v + 4 * h;
+            w[h] = qz.codes(f[0], f[1]) | qz.codes(f[2], f[3]) << 16;
         }
         *reinterpret_cast<uint2*>(p.q + row + c) = make_uint2(w[0], w[1]);
-        if ((tid & 15) == 0) p.scales[(size_t)blockIdx.x * nb + c / kFp8Block] = scale;
+        if ((tid & 15) == 0) p.scales[(size_t)blockIdx.x * nb + c / kFp8Block] = qz.scale;
     }
 }
 

@@ -29,6 +29,8 @@
 // K order (Schedule).
 #include <string.h>
 
+#include <type_traits>
+
 #include "fp8_tiles.cuh"
 
 namespace coli {
@@ -143,66 +145,16 @@ __device__ __forceinline__ void scaled_add(float* acc, const uint32_t (&v)[16], 
 
 // A warp's 32 rows of outputs, one per thread (orow: its row of y, -1 for none): two runs of 64
 // columns, at c0 and c0 + 128, plus the residual, rounded once.  Rows go through shared
-// memory, 128 bytes each at a time, so that 8 neighbouring lanes write (and read the
-// residual's) 128 consecutive bytes; the loads of a piece are under way together.
+// memory, 128 bytes each at a time, so that 8 neighbouring lanes write 128 (64 for bf16 with
+// a residual) consecutive bytes.  The residual was brought into L2 when the tile began; the 8
+// loads of a piece are under way together.
 template <class Y>
-__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, float (&acc)[C],
+__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, const float (&acc)[C],
                                            uint8_t* stage, int lane)
 {
-    constexpr int ES = (int)sizeof(Y), W = 128 / ES;       // columns of a 128-byte piece
-    if (rows % (16 / ES) == 0) {
-        const int r4 = lane >> 3, piece = lane & 7;
-#pragma unroll
-        for (int j0 = 0; j0 < C; j0 += W) {
-            const int col = c0 + (j0 >> 6) * kM + (j0 & 63) + piece * (16 / ES);
-            const bool in = col < rows;
-            if (residual) {
-                uint4 v[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (to >= 0 && in) v[i] = *reinterpret_cast<const uint4*>(residual + (size_t)to * rows + col);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    *reinterpret_cast<uint4*>(stage + (i * 4 + r4) * kPitch + piece * 16) = v[i];
-                __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 8; c++) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(stage + lane * kPitch + c * 16);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        if (ES == 4) {
-                            acc[j0 + 4 * c + e] += __uint_as_float(w[e]);
-                        } else {
-                            acc[j0 + 8 * c + 2 * e] += __uint_as_float(w[e] << 16);
-                            acc[j0 + 8 * c + 2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
-                        }
-                    }
-                }
-            }
-            __syncwarp();        // the pieces staged before have been read
-#pragma unroll
-            for (int c = 0; c < 8; c++) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    w[e] = ES == 4 ? __float_as_uint(acc[j0 + 4 * c + e])
-                                   : bf16x2_bits(acc[j0 + 8 * c + 2 * e], acc[j0 + 8 * c + 2 * e + 1]);
-                *reinterpret_cast<uint4*>(stage + lane * kPitch + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + (i * 4 + r4) * kPitch + piece * 16);
-                if (to >= 0 && in) *reinterpret_cast<uint4*>(y + (size_t)to * rows + col) = v;
-            }
-        }
-    } else {
+    constexpr int ES = (int)sizeof(Y);
+    const int r4 = lane >> 3, piece = lane & 7;
+    if (rows % (16 / ES) != 0) {
         // rows that do not begin on 16 bytes: 32 columns at a time, one lane a column
         float* f = reinterpret_cast<float*>(stage);
         constexpr int P = kPitch / 4;
@@ -226,6 +178,66 @@ __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, in
 #pragma unroll
                 for (int r = 0; r < 8; r++)
                     if (at[r] != ~(size_t)0) y[at[r]] = (Y)v[r];
+            }
+        }
+    } else if (ES == 2 && !residual) {
+#pragma unroll
+        for (int j0 = 0; j0 < C; j0 += 64) {
+            const int col = c0 + (j0 >> 6) * kM + piece * 8;
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                const float* f = acc + j0 + 8 * c;
+                *reinterpret_cast<uint4*>(stage + lane * kPitch + c * 16) = make_uint4(
+                    bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]), bf16x2_bits(f[6], f[7]));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + (i * 4 + r4) * kPitch + piece * 16);
+                if (to >= 0 && col < rows) *reinterpret_cast<uint4*>(y + (size_t)to * rows + col) = v;
+            }
+        }
+    } else {
+        using R = typename std::conditional<ES == 4, float4, uint2>::type;    // 4 columns of the residual
+        auto col_of = [&](int j0) { return c0 + (j0 >> 6) * kM + (j0 & 63) + piece * 4; };
+#pragma unroll
+        for (int j0 = 0; j0 < C; j0 += 32) {
+            R res[8];
+            if (residual) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int r = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
+                    res[i] = R{};
+                    if (r >= 0 && col_of(j0) < rows)
+                        res[i] = *reinterpret_cast<const R*>(residual + (size_t)r * rows + col_of(j0));
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+                *reinterpret_cast<float4*>(stage + lane * kPitch + c * 16) =
+                    make_float4(acc[j0 + 4 * c], acc[j0 + 4 * c + 1], acc[j0 + 4 * c + 2], acc[j0 + 4 * c + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
+                float4 v = *reinterpret_cast<const float4*>(stage + (i * 4 + r4) * kPitch + piece * 16);
+                if (to < 0 || col_of(j0) >= rows) continue;
+                Y* at = y + (size_t)to * rows + col_of(j0);
+                if constexpr (ES == 4) {
+                    if (residual) {
+                        const float4 a = res[i];
+                        v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+                    }
+                    *reinterpret_cast<float4*>(at) = v;
+                } else {
+                    const uint2 a = res[i];
+                    *reinterpret_cast<uint2*>(at) =
+                        make_uint2(bf16x2_bits(v.x + __uint_as_float(a.x << 16), v.y + __uint_as_float(a.x & 0xFFFF0000u)),
+                                   bf16x2_bits(v.z + __uint_as_float(a.y << 16), v.w + __uint_as_float(a.y & 0xFFFF0000u)));
+                }
             }
         }
     }
@@ -384,6 +396,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     orow = a < 0 ? -1 : tl.g.base + tok;
                 }
             }
+            if (MODE == FP8_DENSE && p.residual && orow >= 0 && it.kb1 == p.kb) {
+                // the thread's part of the residual's row into L2
+                const int es = p.y_bf16 ? 2 : 4;
+                const uint8_t* r = reinterpret_cast<const uint8_t*>(p.residual) + (size_t)orow * p.rows * es;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int c = (2 * tl.rb + h) * kM + wg * 64;
+                    for (int o = 0; o < 64 * es; o += 128)
+                        if (c + o / es < p.rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + (size_t)c * es + o));
+                }
+            }
             const float* xs = p.xs + (size_t)(valid ? xrow : 0) * p.kb;
             const float* wbase = tl.g.expert < 0
                                      ? p.ws[1]
@@ -512,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 named_bar(1, kEpi);
                 top = max(top, tops[(wg ^ 1) * kM + row]);
                 named_bar(1, kEpi);      // read before the next tile's
-                const float scale = __fdiv_rn(__uint_as_float(top), kFp8Max);
+                const Quantizer qz(top);
                 const int i0 = tl.rb * kM + wg * 64;
                 if (orow >= 0 && i0 < p.I) {
                     uint4* to = reinterpret_cast<uint4*>(p.hq + (size_t)orow * p.I + i0);
@@ -522,12 +545,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
                             const float* f = acc + j + 4 * e;
-                            w[e] = (uint32_t)code_of(f[0], scale) | (uint32_t)code_of(f[1], scale) << 8 |
-                                   (uint32_t)code_of(f[2], scale) << 16 | (uint32_t)code_of(f[3], scale) << 24;
+                            w[e] = qz.codes(f[0], f[1]) | qz.codes(f[2], f[3]) << 16;
                         }
                         to[j / 16] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    if (wg == 0) p.hs[(size_t)orow * nb + tl.rb] = scale;
+                    if (wg == 0) p.hs[(size_t)orow * nb + tl.rb] = qz.scale;
                 }
             }
         }

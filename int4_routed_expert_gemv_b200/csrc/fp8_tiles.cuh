@@ -278,13 +278,9 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Code of v at a scale (0 at scale 0).
-__device__ __forceinline__ uint8_t code_of(float v, float scale)
-{
-    return (uint8_t)__nv_cvt_float_to_fp8(scale != 0.0f ? __fdiv_rn(v, scale) : 0.0f, __NV_SATFINITE, __NV_E4M3);
-}
-
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) * u: expf and the quotient are within 2 ulp each; the quotient's 0 for 1 + exp(-g)
+// above 2^126 is off by less than the smallest normal number.
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
 
 }  // namespace fp8
 
