@@ -117,15 +117,16 @@ def check(status: int, what: str = "colimoe") -> None:
 
 
 def _p(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _s(stream) -> ctypes.c_void_p:
+def _s(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object around it (3 us of a 10 us call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _dt(x: torch.Tensor) -> int:

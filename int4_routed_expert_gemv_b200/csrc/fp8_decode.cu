@@ -1,10 +1,18 @@
-// Block-scaled e4m3 products for at most 16 tokens (and 16 rows a tile), where reading the
-// weights is all that counts.
+// Block-scaled e4m3 products for at most 16 tokens, where reading the weights is all that
+// counts.
 //
 // A tile is two 128-row blocks of weights (for gate/up: the gate rows and the up rows of the
-// same 128 intermediate columns, which are one scale block of h) by 16 tokens: the weights sit
-// on the MMA's M side, so one token costs a 16-column tile, a thread's accumulators belong to
-// one weight row, and 32 neighbouring lanes write 32 neighbouring outputs.
+// same 128 intermediate columns, which are one scale block of h) by all tokens of the batch:
+// the weights sit on the MMA's M side and the tokens, 16 columns, on its N side, so a
+// thread's accumulators belong to one weight row and 32 neighbouring lanes write 32
+// neighbouring outputs.  Column j is token j in every mode:
+//   DENSE    every tile has the K steps of one product;
+//   GATE_UP  a tile belongs to an expert; it takes the rows of all tokens and keeps the
+//            columns that chose the expert;
+//   DOWN     the K steps of a tile are those of every expert of the union, one expert after
+//            another, shared first: the combine is the accumulation, with the routing weight
+//            as one more factor of a column's scale, and the columns that did not choose an
+//            expert masked.  So y is written once, in one launch, in one fixed order.
 //
 // CTA (one per SM), 12 warps:
 //   warps 0-7   two warpgroups: scaled accumulation of each K step of 128, and the tile's
@@ -26,90 +34,207 @@ namespace {
 
 using namespace fp8;
 
-constexpr int NT = 16;                  // tokens of a tile
+constexpr int NT = 16;                  // columns: tokens
+constexpr int C = NT / 2;               // columns of a thread, per row block
 constexpr int kStages = 6;
 constexpr uint32_t kStage = 2 * kM * 128 + NT * 128;
 constexpr int kBufs = 4;                // accumulator buffers in tensor memory
 constexpr uint32_t kTmem = kBufs * 2 * NT;
 constexpr int kLeast = 2;               // K steps of a run at least
+constexpr int kJoin = 3;                // what joining the parts of a tile costs, in K steps
+constexpr int kMaxPos = NT * 32;        // positions of the union lists: 16 tokens, top-32
 constexpr uint32_t kSite = 60;
-constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + (size_t)kSlots * 2 * NT * 4 + 2 * 4 * (NT / 2) * 4 +
-                         (kMaxGroups + 3) / 4 * 4 * 4 + 16 + 64 + 512;
+
+struct Tables {
+    int expert[kMaxGroups], base[kMaxGroups], count[kMaxGroups];
+    int pos[kMaxPos];                   // t * k + slot of each list position (-1: not of this batch)
+    float wt[kMaxPos];                  // its routing weight
+};
+
+struct Smem {
+    uint8_t stage[kStages][kStage];
+    float scale[kSlots][2][NT];
+    uint32_t mask[kSlots];              // DOWN: columns of the step's expert
+    uint32_t top[2][4][C];              // maxima of the SwiGLU rows, by warp
+    int col_pos[NT];
+    uint32_t tmem;
+    int n_groups, last;
+    uint64_t full[kStages];             // tiles landed
+    uint64_t empty[kStages];            // MMAs done with the stage
+    uint64_t acc_full[kBufs];           // MMA commit
+    uint64_t acc_empty[kBufs];          // read by every accumulating warp
+    uint64_t sc_full[kSlots], sc_empty[kSlots];
+    uint64_t mma_done;
+    Tables t;
+};
+constexpr size_t kSmem = sizeof(Smem) + 1024;
+
+// Four rows of a 2-D map (box one row high) into four consecutive 128-byte rows.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int x, int4 y, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
+// A run of K steps of one expert's matrix within an item.
+struct Segment {
+    int g, rb;         // group, row block
+    int k0, k1;        // K steps
+};
+
+// The segments of an item, in order.
+template <int MODE>
+struct Segments {
+    int rb, g, u, u1, kb;
+    __device__ Segments(const Params& p, const Item& it)
+    {
+        kb = p.kb;
+        u = it.kb0;
+        u1 = it.kb1;
+        rb = MODE == FP8_GATE_UP ? it.tile % p.rb : it.tile;
+        g = MODE == FP8_GATE_UP ? it.tile / p.rb : 0;
+    }
+    __device__ bool next(Segment& s)
+    {
+        if (u >= u1) return false;
+        const int skip = MODE == FP8_DOWN ? u / kb : 0;
+        s.g = g + skip;
+        s.rb = rb;
+        s.k0 = u - skip * kb;
+        s.k1 = min(kb, s.k0 + u1 - u);
+        u += s.k1 - s.k0;
+        return true;
+    }
+};
+
+// List position of token j in group g (its row of h), -1 if the group has none.
+__device__ __forceinline__ int row_of(const Params& p, const Tables& t, int g, int j)
+{
+    if (j >= p.T) return -1;
+    if (t.expert[g] < 0) return t.base[g] + j;
+    int r = -1;
+    for (int l = 0; l < t.count[g]; l++) {
+        const int a = t.pos[t.base[g] + l];
+        if (a >= 0 && a / p.k == j) r = t.base[g] + l;
+    }
+    return r;
+}
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_constant__ Params p)
 {
-    constexpr int C = NT / 2;      // columns of a thread, per row block
-    // The experts' first product takes all tokens' rows for every expert and keeps the
-    // columns that chose it.
-    constexpr bool kAllTokens = MODE == FP8_GATE_UP;
-
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* scale_ring = reinterpret_cast<float*>(smem + kStages * (size_t)kStage);
-    uint32_t* tops = reinterpret_cast<uint32_t*>(scale_ring + kSlots * 2 * NT);
-    int* first = reinterpret_cast<int*>(tops + 2 * 4 * C);              // token tiles before each group
-    int* flags = first + (kMaxGroups + 3) / 4 * 4;                      // [0] groups [1] tiles [2] last [3] tmem
-    int* col_pos = flags + 4;                                           // [16]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(col_pos + 16);
-    uint64_t* full = bars;                       // [kStages] tiles landed
-    uint64_t* empty = full + kStages;         // [kStages] MMAs done with the stage
-    uint64_t* acc_full = empty + kStages;     // [kBufs] MMA commit
-    uint64_t* acc_empty = acc_full + kBufs;   // [kBufs] read by every accumulating warp
-    uint64_t* sc_full = acc_empty + kBufs;    // [kSlots]
-    uint64_t* sc_empty = sc_full + kSlots;       // [kSlots]
-    uint64_t* mma_done = sc_empty + kSlots;
-
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
     if (tid == 0) {
         for (int s = 0; s < kStages; s++) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
         }
         for (int b = 0; b < kBufs; b++) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], kEpi / 32);
+            mbar_init(&sm.acc_full[b], 1);
+            mbar_init(&sm.acc_empty[b], kEpi / 32);
         }
         for (int s = 0; s < kSlots; s++) {
-            mbar_init(&sc_full[s], 1);
-            mbar_init(&sc_empty[s], kEpi / 32);
+            mbar_init(&sm.sc_full[s], 1);
+            mbar_init(&sm.sc_empty[s], kEpi / 32);
         }
-        mbar_init(mma_done, 1);
+        mbar_init(&sm.mma_done, 1);
         fence_barrier_init();
     }
-    if (warp == 9) tmem_alloc(reinterpret_cast<uint32_t*>(&flags[3]), kTmem);
-    if (warp == 8) plan_tiles<MODE>(p, NT, lane, first, &flags[0], &flags[1]);
+    if (warp == 9) tmem_alloc(&sm.tmem, kTmem);
+    if (warp == 8) {
+        if (lane < 2) prefetch_map(&p.w[lane]);
+        else if (lane == 2) prefetch_map(&p.x[0]);
+        // the groups: loads that do not wait for one another
+        int ng = 1;
+        if (MODE != FP8_DENSE) {
+            const int nu = *p.n_union;
+            for (int u = lane; u < p.E; u += 32) {
+                const int id = p.union_ids[u], b = p.offsets[u], e = p.offsets[u + 1];
+                const bool bad = id < 0 || id >= p.E || b < 0 || e < b || e > p.T * p.k;
+                const int g = p.n_shared + u;
+                sm.t.expert[g] = bad ? 0 : id;
+                sm.t.base[g] = bad ? 0 : b;
+                sm.t.count[g] = bad ? 0 : e - b;
+                if (bad && u < nu) set_flag(p.status, DEV_BAD_INDEX);
+                if (u >= nu) break;
+            }
+            if ((nu < 0 || nu > p.E) && lane == 0) set_flag(p.status, DEV_BAD_INDEX);
+            ng = p.n_shared + min(max(nu, 0), p.E);
+        }
+        if (lane == 0) {
+            if (MODE != FP8_DENSE && p.n_shared) {
+                sm.t.expert[0] = -1;
+                sm.t.base[0] = p.T * p.k;
+                sm.t.count[0] = p.T;
+            } else if (MODE == FP8_DENSE || ng == 0) {
+                // DOWN without any expert: one group that no column chose
+                sm.t.expert[0] = sm.t.base[0] = sm.t.count[0] = 0;
+            }
+            sm.n_groups = ng;
+        }
+    } else if (MODE != FP8_DENSE && warp < 8) {
+        for (int i = tid; i < p.T * p.k; i += kEpi) {
+            const int a = position_of(p, i);
+            sm.t.pos[i] = a;
+            if (MODE == FP8_DOWN) sm.t.wt[i] = a < 0 ? 0.0f : __ldg(p.wts + a);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = (uint32_t)flags[3];
-    const int n_groups = flags[0];
+    const uint32_t tmem = sm.tmem;
     Schedule sch;
-    sch.init(flags[1], p.kb, (int)gridDim.x, (int)blockIdx.x, kLeast);
+    const int ng = sm.n_groups, steps = MODE == FP8_DOWN ? max(ng, 1) * p.kb : p.kb;
+    sch.init(MODE == FP8_GATE_UP ? ng * p.rb : p.rb, steps, (int)gridDim.x, (int)blockIdx.x, kLeast, kJoin);
     bool dead = false;
     Item it;
+    Segment sg;
 
     if (warp == 8) {
         // ------------------------------- TMA producer -----------------------------------
         uint32_t n = 0;
         while (sch.next(it)) {
-            const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
-            const int shared = tl.g.expert < 0 ? 1 : 0;
-            const CUtensorMap* wm = &p.w[shared];
-            const int z = shared ? 0 : tl.g.expert;
-            const int r0 = p.row_off + (MODE == FP8_GATE_UP ? tl.rb * kM : tl.rb * 2 * kM);
-            const int r1 = MODE == FP8_GATE_UP ? r0 + p.I : r0 + kM;
-            const int row0 = MODE == FP8_DENSE ? tl.t0 : kAllTokens ? 0 : tl.g.base + tl.t0;
-            for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
-                const int s = n % kStages;
-                if (!dead && !mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
-                if (dead) continue;
-                uint8_t* st = smem + (size_t)s * kStage;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[s], kStage);
-                    tma_load_3d(st, wm, kb * 128, r0, z, &full[s]);
-                    tma_load_3d(st + kM * 128, wm, kb * 128, r1, z, &full[s]);
-                    tma_load_2d(st + 2 * kM * 128, &p.x[0], kb * 128, row0, &full[s]);
+            Segments<MODE> segs(p, it);
+            while (segs.next(sg)) {
+                const int expert = sm.t.expert[sg.g];
+                const CUtensorMap* wm = &p.w[expert < 0 ? 1 : 0];
+                const int z = max(expert, 0);
+                const int r0 = MODE == FP8_GATE_UP ? sg.rb * kM : sg.rb * 2 * kM;
+                const int r1 = MODE == FP8_GATE_UP ? r0 + p.I : r0 + kM;
+                int4 rows = make_int4(0, 0, 0, 0);
+                if (MODE == FP8_DOWN) {
+                    // any row (0) for the columns that are masked
+                    const int r = lane < NT ? max(row_of(p, sm.t, sg.g, lane), 0) : 0;
+                    rows.x = __shfl_sync(0xffffffffu, r, (lane & 3) * 4);
+                    rows.y = __shfl_sync(0xffffffffu, r, (lane & 3) * 4 + 1);
+                    rows.z = __shfl_sync(0xffffffffu, r, (lane & 3) * 4 + 2);
+                    rows.w = __shfl_sync(0xffffffffu, r, (lane & 3) * 4 + 3);
+                }
+                for (int kb = sg.k0; kb < sg.k1; kb++, n++) {
+                    const int s = n % kStages;
+                    if (!dead && !mbar_wait(&sm.empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
+                    if (dead) continue;
+                    uint8_t* st = sm.stage[s];
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sm.full[s], kStage);
+                        tma_load_3d(st, wm, kb * 128, r0, z, &sm.full[s]);
+                        tma_load_3d(st + kM * 128, wm, kb * 128, r1, z, &sm.full[s]);
+                        if (MODE != FP8_DOWN) tma_load_2d(st + 2 * kM * 128, &p.x[0], kb * 128, 0, &sm.full[s]);
+                    }
+                    __syncwarp();
+                    if (MODE == FP8_DOWN && lane < NT / 4)
+                        tma_gather4(st + 2 * kM * 128 + lane * 512, &p.x[0], kb * 128, rows, &sm.full[s]);
                 }
             }
         }
@@ -118,219 +243,226 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
             const uint32_t last = n < (uint32_t)kStages ? n : (uint32_t)kStages;
             for (uint32_t i = 0; i < last; i++) {
                 const uint32_t m = n - 1 - i;
-                mbar_wait(&full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
+                mbar_wait(&sm.full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
             }
         }
     } else if (warp == 9) {
         // ------------------------------- MMA issuer -------------------------------------
         if (lane == 0) {
+            const uint32_t idesc = idesc_e4m3(kM, NT);
             uint32_t n = 0;
             while (sch.next(it)) {
-                const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
-                const uint32_t idesc = idesc_e4m3(kM, NT);
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int s = n % kStages, b = n % kBufs;
-                    if (!dead && !mbar_wait(&acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
-                    if (!dead && !mbar_wait(&full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
+                    if (!dead && !mbar_wait(&sm.acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
+                    if (!dead && !mbar_wait(&sm.full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
                     tc_fence_after();
                     if (!dead) {
-                        const uint8_t* st = smem + (size_t)s * kStage;
+                        const uint8_t* st = sm.stage[s];
                         const uint64_t bd = sw128_desc(st + 2 * kM * 128);
 #pragma unroll
                         for (int m = 0; m < 2; m++) {
                             const uint64_t ad = sw128_desc(st + m * kM * 128);
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)      // 32 e4m3 values = 32 bytes per MMA
-                                umma_e4m3(tmem + (uint32_t)(b * 2 * NT + m * NT), ad + 2 * kk, bd + 2 * kk, idesc,
-                                          kk != 0);
+                                umma_e4m3(tmem + (uint32_t)(b * 2 * NT + m * NT), ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
                         }
                     }
-                    umma_commit(&empty[s]);
-                    umma_commit(&acc_full[b]);
+                    umma_commit(&sm.empty[s]);
+                    umma_commit(&sm.acc_full[b]);
                 }
             }
-            umma_commit(mma_done);
-            mbar_wait(mma_done, 0, p.status, kSite + 5);
+            umma_commit(&sm.mma_done);
+            mbar_wait(&sm.mma_done, 0, p.status, kSite + 5);
         }
     } else if (warp == 10) {
         // ------------------------------- scale products ---------------------------------
+        // lane m * 16 + j: row block m, column j; K steps are fetched B at a time, a batch ahead
+        constexpr int B = 4;
+        const int m = lane >> 4, j = lane & 15;
+        const int nb = fp8_blocks(p.rows);     // row blocks of a matrix
         uint32_t n = 0;
-        ScaleWarp<NT, 2, 4> sw;
         while (sch.next(it)) {
-            const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
-            const int row = lane >= (kAllTokens ? p.T : tl.n) ? -1
-                            : MODE == FP8_DENSE               ? tl.t0 + lane
-                            : kAllTokens                      ? lane
-                                                              : tl.g.base + tl.t0 + lane;
-            sw.xrow[0] = row < 0 || lane >= NT ? nullptr : p.xs + (size_t)row * p.kb;
-            const float* wbase = tl.g.expert < 0 ? p.ws[1]
-                                                 : reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws[0]) +
-                                                                                  (uint64_t)tl.g.expert * p.ws_stride);
-            const int nb = fp8_blocks(p.rows);     // row blocks of the matrix
-            const int b0 = MODE == FP8_GATE_UP ? tl.rb : 2 * tl.rb;
-            sw.w[0] = wbase + (size_t)b0 * p.kb;
-            sw.w[1] = MODE == FP8_GATE_UP ? sw.w[0] + (size_t)nb * p.kb : b0 + 1 < nb ? sw.w[0] + p.kb : nullptr;
-            sw.run(it, lane, scale_ring, sc_full, sc_empty, n, dead, p.status, kSite + 6);
+            Segments<MODE> segs(p, it);
+            while (segs.next(sg)) {
+                const int expert = sm.t.expert[sg.g];
+                const int row = MODE == FP8_DOWN ? row_of(p, sm.t, sg.g, j) : j < p.T ? j : -1;
+                const float wt = MODE != FP8_DOWN || expert < 0 || row < 0 ? 1.0f : sm.t.wt[row];
+                const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu;
+                const float* xs = p.xs + (size_t)max(row, 0) * p.kb;
+                const float* wb = expert < 0 ? p.ws[1]
+                                             : reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws[0]) +
+                                                                              (uint64_t)expert * p.ws_stride);
+                const int blk = MODE == FP8_GATE_UP ? sg.rb + m * nb : min(2 * sg.rb + m, nb - 1);
+                const float* ws = wb + (size_t)blk * p.kb;
+                float xv[B], wv[B];
+                auto fetch = [&](int kb) {
+#pragma unroll
+                    for (int i = 0; i < B; i++) {
+                        const int k = min(kb + i, sg.k1 - 1);
+                        xv[i] = __ldg(xs + k);
+                        wv[i] = __ldg(ws + k);
+                    }
+                };
+                fetch(sg.k0);
+                for (int kb = sg.k0; kb < sg.k1; kb += B) {
+                    float s[B];
+#pragma unroll
+                    for (int i = 0; i < B; i++) s[i] = row < 0 ? 0.0f : xv[i] * wv[i] * wt;
+                    if (kb + B < sg.k1) fetch(kb + B);
+#pragma unroll
+                    for (int i = 0; i < B; i++) {
+                        if (kb + i >= sg.k1) break;
+                        const int slot = n % kSlots;
+                        if (!dead && !mbar_wait(&sm.sc_empty[slot], ((n / kSlots) & 1) ^ 1, p.status, kSite + 6)) dead = true;
+                        sm.scale[slot][m][j] = s[i];
+                        if (MODE == FP8_DOWN && lane == 0) sm.mask[slot] = mask;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.sc_full[slot]);
+                        n++;
+                    }
+                }
+            }
         }
     } else if (warp < 8) {
         // ------------------------- scaled accumulation, outputs -------------------------
         const int wg = warp >> 2, q = warp & 3;     // warpgroup, TMEM lane quarter
         const int row = q * 32 + lane;              // weight row within a 128-row block
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(wg * C);
-        uint64_t acc[2][C / 2];
-        float* accf = reinterpret_cast<float*>(acc);
+        const int mine = min(max(p.T - wg * C, 0), C);   // columns of this warpgroup in use
+        float acc[2][C];
         uint32_t n = 0;
         while (sch.next(it)) {
-            const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
-            const int ncol = kAllTokens ? p.T : tl.n;         // columns of the tile in use
-            const int mine = min(max(ncol - wg * C, 0), C);   // this warpgroup's
 #pragma unroll
             for (int m = 0; m < 2; m++)
 #pragma unroll
-                for (int j = 0; j < C / 2; j++) acc[m][j] = 0;
+                for (int j = 0; j < C; j++) acc[m][j] = 0.0f;
             for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                 const int b = n % kBufs, s = n % kSlots;
-                if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
-                if (!dead && !mbar_wait(&sc_full[s], (n / kSlots) & 1, p.status, kSite + 8)) dead = true;
+                if (!dead && !mbar_wait(&sm.sc_full[s], (n / kSlots) & 1, p.status, kSite + 8)) dead = true;
+                if (!dead && !mbar_wait(&sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
                 tc_fence_after();
-                const float* sc = scale_ring + s * 2 * NT + wg * C;
                 if (mine > 0) {
                     uint32_t v[2][C];
 #pragma unroll
                     for (int m = 0; m < 2; m++) tmem_ld8(lane_addr + (uint32_t)(b * 2 * NT + m * NT), v[m]);
-                    tmem_wait_ld();
+                    float sc[2][C];
 #pragma unroll
                     for (int m = 0; m < 2; m++)
 #pragma unroll
                         for (int j = 0; j < C; j += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(sc + m * NT + j);
-                            acc[m][j / 2] = ffma2(pk2(v[m][j], v[m][j + 1]), pk2f(f.x, f.y), acc[m][j / 2]);
-                            acc[m][j / 2 + 1] = ffma2(pk2(v[m][j + 2], v[m][j + 3]), pk2f(f.z, f.w), acc[m][j / 2 + 1]);
+                            const float4 f = *reinterpret_cast<const float4*>(&sm.scale[s][m][wg * C + j]);
+                            sc[m][j] = f.x;
+                            sc[m][j + 1] = f.y;
+                            sc[m][j + 2] = f.z;
+                            sc[m][j + 3] = f.w;
                         }
+                    const uint32_t mask = MODE == FP8_DOWN ? sm.mask[s] >> (wg * C) : 0xFFu;
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int m = 0; m < 2; m++)
+#pragma unroll
+                        for (int j = 0; j < C; j++)
+                            if (MODE != FP8_DOWN || (mask >> j & 1))
+                                acc[m][j] = fmaf(__uint_as_float(v[m][j]), sc[m][j], acc[m][j]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&acc_empty[b]);
-                    mbar_arrive(&sc_empty[s]);
+                    mbar_arrive(&sm.acc_empty[b]);
+                    mbar_arrive(&sm.sc_empty[s]);
                 }
             }
-            if (it.kb1 - it.kb0 < p.kb) {
+            if (it.kb1 - it.kb0 < steps) {
                 // part of a tile: store the sums; the last part to arrive adds all of them up
-                const int o0 = sch.owner(it.tile * p.kb), o1 = sch.owner(it.tile * p.kb + p.kb - 1);
-                const size_t slot = (size_t)(2 * blockIdx.x + (it.kb0 == 0 ? 1 : 0)) * 2 * C * kEpi;
-                float4* dst = reinterpret_cast<float4*>(p.partial + slot);
+                const int o0 = sch.owner(it.tile * steps), o1 = sch.owner(it.tile * steps + steps - 1);
+                float* dst = p.partial + (size_t)(2 * blockIdx.x + (it.kb0 == 0 ? 1 : 0)) * 2 * C * kEpi + tid;
 #pragma unroll
                 for (int m = 0; m < 2; m++)
 #pragma unroll
-                    for (int j = 0; j < C / 2; j += 2) {
-                        const float2 a = unpk2(acc[m][j]), b2 = unpk2(acc[m][j + 1]);
-                        if (2 * j < mine)
-                            __stcg(dst + (m * (C / 4) + j / 2) * kEpi + tid, make_float4(a.x, a.y, b2.x, b2.y));
-                    }
+                    for (int j = 0; j < C; j++)
+                        if (j < mine) __stcg(dst + (m * C + j) * kEpi, acc[m][j]);
                 __threadfence();
                 named_bar(1, kEpi);
                 if (tid == 0) {
                     const uint32_t old = atomicAdd(&p.tickets[o0], 1u);
                     const bool last = old == (uint32_t)(o1 - o0);
                     if (last) p.tickets[o0] = 0;
-                    flags[2] = last;
+                    sm.last = last;
                 }
                 named_bar(1, kEpi);
-                if (!flags[2]) continue;
+                if (!sm.last) continue;
                 __threadfence();
 #pragma unroll
                 for (int m = 0; m < 2; m++)
 #pragma unroll
-                    for (int j = 0; j < C / 2; j++) acc[m][j] = 0;
+                    for (int j = 0; j < C; j++) acc[m][j] = 0.0f;
                 for (int o = o0; o <= o1; o++) {
-                    const size_t from = (size_t)(2 * o + (o == o0 ? 1 : 0)) * 2 * C * kEpi;
-                    const float4* src = reinterpret_cast<const float4*>(p.partial + from);
+                    const float* src = p.partial + (size_t)(2 * o + (o == o0 ? 1 : 0)) * 2 * C * kEpi + tid;
 #pragma unroll
                     for (int m = 0; m < 2; m++)
 #pragma unroll
-                        for (int j = 0; j < C / 2; j += 2)
-                            if (2 * j < mine) {
-                                const float4 f = __ldcg(src + (m * (C / 4) + j / 2) * kEpi + tid);
-                                acc[m][j] = fadd2(acc[m][j], pk2f(f.x, f.y));
-                                acc[m][j + 1] = fadd2(acc[m][j + 1], pk2f(f.z, f.w));
-                            }
+                        for (int j = 0; j < C; j++)
+                            if (j < mine) acc[m][j] += __ldcg(src + (m * C + j) * kEpi);
                 }
             }
-            if (MODE == FP8_DENSE) {
+            if (MODE != FP8_GATE_UP) {
 #pragma unroll
                 for (int m = 0; m < 2; m++) {
-                    const int r = tl.rb * 2 * kM + m * kM + row;
+                    const int r = it.tile * 2 * kM + m * kM + row;
                     if (r >= p.rows) continue;
+                    const size_t o = (size_t)(wg * C) * p.rows + r;
+                    if (p.residual) {
+                        float res[C];      // loads under way together: the stores may alias them
+#pragma unroll
+                        for (int j = 0; j < C; j++)
+                            res[j] = j >= mine    ? 0.0f
+                                     : p.y_bf16 ? __bfloat162float(
+                                                      reinterpret_cast<const __nv_bfloat16*>(p.residual)[o + (size_t)j * p.rows])
+                                                : reinterpret_cast<const float*>(p.residual)[o + (size_t)j * p.rows];
+#pragma unroll
+                        for (int j = 0; j < C; j++) acc[m][j] += res[j];
+                    }
 #pragma unroll
                     for (int j = 0; j < C; j++) {
                         if (j >= mine) break;
-                        const size_t o = (size_t)(tl.t0 + wg * C + j) * p.rows + r;
-                        float v = accf[m * C + j];
-                        if (p.y_bf16) {
-                            if (p.residual) v += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[o]);
-                            reinterpret_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
-                        } else {
-                            if (p.residual) v += reinterpret_cast<const float*>(p.residual)[o];
-                            reinterpret_cast<float*>(p.y)[o] = v;
-                        }
-                    }
-                }
-            } else if (MODE == FP8_DOWN) {
-#pragma unroll
-                for (int j = 0; j < C; j++) {
-                    if (j >= mine) break;
-                    const int pos = tl.g.base + tl.t0 + wg * C + j;
-                    const int a = tl.g.expert < 0 ? pos : position_of(p, pos);
-                    if (a < 0) {
-                        if (tid == 0) set_flag(p.status, DEV_BAD_INDEX);
-                        continue;
-                    }
-                    if (tl.rb == 0 && row == 0 && tl.g.expert >= 0) p.present[a] = 1;
-#pragma unroll
-                    for (int m = 0; m < 2; m++) {
-                        const int r = tl.rb * 2 * kM + m * kM + row;
-                        if (r < p.rows) p.z[(size_t)a * p.rows + r] = accf[m * C + j];
+                        if (p.y_bf16)
+                            reinterpret_cast<__nv_bfloat16*>(p.y)[o + (size_t)j * p.rows] = __float2bfloat16_rn(acc[m][j]);
+                        else
+                            reinterpret_cast<float*>(p.y)[o + (size_t)j * p.rows] = acc[m][j];
                     }
                 }
             } else {
                 // SwiGLU; its 128 rows are one scale block of h
-                const int i = tl.rb * kM + row;
-                uint32_t* top = tops + (wg * 4 + q) * C;
-                int* cp = col_pos + wg * C;       // rows of h of this warpgroup's columns
-                if (row < C) cp[row] = -1;
-                named_bar(2 + wg, 128);
-                for (int l = row; l < tl.g.count; l += 128) {
-                    const int a = tl.g.expert < 0 ? l * p.k : position_of(p, tl.g.base + l);
-                    if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                    const int t = a < 0 ? -1 : a / p.k;
-                    if (t >= wg * C && t < wg * C + C) cp[t - wg * C] = tl.g.base + l;
-                }
+                const int g = it.tile / p.rb, rb = it.tile - g * p.rb, i = rb * kM + row;
+                if (row < C) sm.col_pos[wg * C + row] = row_of(p, sm.t, g, wg * C + row);
 #pragma unroll
                 for (int j = 0; j < C; j++) {
                     if (j >= mine) break;
-                    const float gv = accf[j], uv = accf[C + j];
-                    const float h = i < p.I ? swiglu(gv, uv) : 0.0f;
-                    accf[j] = h;
-                    const uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu);
-                    if (lane == 0) top[j] = t;
+                    acc[0][j] = i < p.I ? swiglu(acc[0][j], acc[1][j]) : 0.0f;
+                    const uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][j]) & 0x7FFFFFFFu);
+                    if (lane == 0) sm.top[wg][q][j] = t;
                 }
                 named_bar(2 + wg, 128);
                 const int ib = fp8_blocks(p.I);
 #pragma unroll
                 for (int j = 0; j < C; j++) {
                     if (j >= mine) break;
-                    const uint32_t* t4 = tops + wg * 4 * C + j;
-                    const uint32_t t = max(max(t4[0], t4[C]), max(t4[2 * C], t4[3 * C]));
-                    const Quantizer qz(t);
-                    const int pos = cp[j];
+                    const int pos = sm.col_pos[wg * C + j];
                     if (pos < 0 || i >= p.I) continue;
-                    p.hq[(size_t)pos * p.I + i] = (uint8_t)qz.codes(accf[j], 0.0f);
-                    if (row == 0) p.hs[(size_t)pos * ib + tl.rb] = qz.scale;
+                    const Quantizer qz(
+                        max(max(sm.top[wg][0][j], sm.top[wg][1][j]), max(sm.top[wg][2][j], sm.top[wg][3][j])));
+                    p.hq[(size_t)pos * p.I + i] = (uint8_t)qz.codes(acc[0][j], 0.0f);
+                    if (row == 0) p.hs[(size_t)pos * ib + rb] = qz.scale;
                 }
                 named_bar(2 + wg, 128);      // the maxima are read before the next tile's
             }
         }
+        // list positions that are none of the batch's
+        if (MODE != FP8_DENSE && blockIdx.x == 0)
+            for (int g = p.n_shared; g < ng; g++)
+                for (int l = tid; l < sm.t.count[g]; l += kEpi)
+                    if (sm.t.pos[sm.t.base[g] + l] < 0) set_flag(p.status, DEV_BAD_INDEX);
     }
     tc_fence_before();
     __syncthreads();
@@ -343,8 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 template <int MODE>
 cudaError_t launch(const Params& p, int grid, cudaStream_t s)
 {
-    const cudaError_t e =
-        cudaFuncSetAttribute(fp8_decode_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const cudaError_t e = allow_smem<fp8_decode_kernel<MODE>>(kSmem);
     if (e != cudaSuccess) return e;
     fp8_decode_kernel<MODE><<<grid, kThreads, kSmem, s>>>(p);
     return cudaGetLastError();

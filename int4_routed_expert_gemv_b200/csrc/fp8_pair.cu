@@ -48,6 +48,7 @@ constexpr int kBufs = 2;
 constexpr uint32_t kTmem = kBufs * 256;
 constexpr int kBox = 64;                          // rows of a token box
 constexpr int kLeast = 6;                         // K steps of a run at least
+constexpr int kJoin = 12;                         // what joining the parts of a tile costs, in K steps
 constexpr int kPitch = 144;                       // bytes of a staged row: 128 and a gap
 constexpr size_t kOut = (size_t)kEpi * kPitch;
 constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 2 * kM * 4 +
@@ -291,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = (uint32_t)flags[3];
     const int n_groups = flags[0];
     Schedule sch;
-    sch.init(flags[1], p.kb, (int)n_clusters(), (int)cluster_id(), kLeast);
+    sch.init(flags[1], p.kb, (int)n_clusters(), (int)cluster_id(), kLeast, kJoin);
     bool dead = false;
     Item it;
 
@@ -566,8 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int MODE>
 cudaError_t launch(const Params& p, int grid, cudaStream_t s)
 {
-    const cudaError_t e =
-        cudaFuncSetAttribute(fp8_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const cudaError_t e = allow_smem<fp8_pair_kernel<MODE>>(kSmem);
     if (e != cudaSuccess) return e;
     fp8_pair_kernel<MODE><<<grid, kThreads, kSmem, s>>>(p);
     return cudaGetLastError();

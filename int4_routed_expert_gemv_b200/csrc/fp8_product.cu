@@ -5,7 +5,8 @@
 //
 //   DENSE    y = round(residual + out)
 //   GATE_UP  row p of the union lists: h = silu(g) * u, then codes and scales of h
-//   DOWN     z[t * k + slot] = out (fp32); a second launch adds residual, the shared row and
+//   DOWN     up to 16 tokens the combine is part of the product (fp8_decode.cu); above,
+//            z[t * k + slot] = out (fp32), and a second launch adds residual, the shared row and
 //            the routing-weighted rows of each token in a fixed order
 #include <string.h>
 
@@ -110,7 +111,7 @@ size_t fp8_scratch_bytes(int mode, int64_t T, int H, int k, int n_shared)
 {
     size_t n = partial_bytes(T);
     if (mode == FP8_GATE_UP && T > kDecodeTokens) n += up((size_t)T * k * H);
-    if (mode == FP8_DOWN) n += up((size_t)T * k) + up((size_t)T * (k + n_shared) * H * sizeof(float));
+    if (mode == FP8_DOWN && T > kDecodeTokens) n += up((size_t)T * k) + up((size_t)T * (k + n_shared) * H * sizeof(float));
     return n;
 }
 
@@ -119,7 +120,8 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     Params p;
     memset(&p, 0, sizeof(p));
     const bool decode = a.T <= kDecodeTokens;
-    const int box = decode ? 16 : 64;     // rows of a token box
+    // rows of a token box (1: rows gathered one by one)
+    const int box = !decode ? 64 : a.mode == FP8_DOWN ? 1 : 16;
     uint8_t* gathered = a.scratch + partial_bytes(a.T);
     bool ok = true;
     if (a.mode == FP8_DENSE) {
@@ -182,7 +184,8 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    if (a.mode != FP8_DOWN) return product();
+    p.wts = a.wts;
+    if (a.mode != FP8_DOWN || decode) return product();
     uint8_t* at = a.scratch + partial_bytes(a.T);
     p.present = at;
     p.z = reinterpret_cast<float*>(at + up((size_t)a.T * a.k));

@@ -23,10 +23,10 @@ struct Params {
     int K, kb;                    // contraction length and its scale blocks
     int rows, rb;                 // output rows of a matrix, 256-row (or gate/up pair) blocks
     int T, k, E, n_shared, I;
-    int row_off;                  // rows before the wanted matrix inside a blob's map
     const float* ws[2];           // dense: scales; experts: first blob's scales, shared's
     uint64_t ws_stride;           // bytes between experts' scales
     const float* xs;              // scales of the token codes
+    const float* wts;             // DOWN: routing weights
     const int32_t* union_ids;
     const int32_t* n_union;
     const int32_t* offsets;
@@ -119,14 +119,18 @@ struct Schedule {
     int per, more, n_run;         // units per run, runs with one more, runs
     int u, u1, t;
 
-    __device__ void init(int tiles_, int kb_, int G_, int c_, int least)
+    // join: what joining the parts of a tile costs, in K steps.  Splitting has to save more;
+    // a worker alone streams a quarter faster than all of them together.
+    __device__ void init(int tiles_, int kb_, int G_, int c_, int least, int join)
     {
         tiles = tiles_;
         kb = kb_;
         G = G_;
         c = c_;
         const int rest = tiles % G;
-        split = rest == 0 ? 0 : tiles < G ? tiles : rest + G;
+        const int waves = (tiles + G - 1) / G;
+        const int whole = waves == 1 ? kb * max(tiles, 4 * G / 5) / G : waves * kb;
+        split = rest == 0 || whole <= (int)((int64_t)tiles * kb / G) + join ? 0 : tiles < G ? tiles : rest + G;
         const int units = split * kb;
         n_run = min(G, max(1, units / least));
         per = units / n_run;
@@ -220,58 +224,6 @@ __device__ __forceinline__ void plan_tiles(const Params& p, int nt, int lane, in
     }
 }
 
-// Warp that forms the scale products of a ring slot: columns lane, lane + 32, .. below NT
-// (xrow[l]: a column's scales, null for a column without a token) times W weight scales.
-// K steps are fetched B at a time, one batch ahead.
-template <int NT, int W, int B>
-struct ScaleWarp {
-    static constexpr int L = (NT + 31) / 32;
-    const float* xrow[L];
-    const float* w[W];
-
-    __device__ __forceinline__ void run(const Item& it, int lane, float* ring, uint64_t* full, uint64_t* empty,
-                                        uint32_t& n, bool& dead, uint32_t* status, uint32_t site)
-    {
-        float xv[B][L], wv[B][W];
-        auto fetch = [&](int kb) {
-#pragma unroll
-            for (int i = 0; i < B; i++) {
-                const bool in = kb + i < it.kb1;
-#pragma unroll
-                for (int l = 0; l < L; l++) xv[i][l] = in && xrow[l] ? __ldg(xrow[l] + kb + i) : 0.0f;
-#pragma unroll
-                for (int m = 0; m < W; m++) wv[i][m] = in && w[m] ? __ldg(w[m] + kb + i) : 0.0f;
-            }
-        };
-        fetch(it.kb0);
-        for (int kb = it.kb0; kb < it.kb1; kb += B) {
-            float s[B][W][L];
-#pragma unroll
-            for (int i = 0; i < B; i++)
-#pragma unroll
-                for (int m = 0; m < W; m++)
-#pragma unroll
-                    for (int l = 0; l < L; l++) s[i][m][l] = xv[i][l] * wv[i][m];
-            if (kb + B < it.kb1) fetch(kb + B);
-#pragma unroll
-            for (int i = 0; i < B; i++) {
-                if (kb + i >= it.kb1) break;
-                const int slot = n % kSlots;
-                if (!dead && !mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, status, site)) dead = true;
-                float* d = ring + slot * W * NT;
-#pragma unroll
-                for (int m = 0; m < W; m++)
-#pragma unroll
-                    for (int l = 0; l < L; l++)
-                        if (lane + 32 * l < NT) d[m * NT + lane + 32 * l] = s[i][m][l];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[slot]);
-                n++;
-            }
-        }
-    }
-};
-
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
 {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -281,6 +233,20 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
 // silu(g) * u: expf and the quotient are within 2 ulp each; the quotient's 0 for 1 + exp(-g)
 // above 2^126 is off by less than the smallest normal number.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+
+// Dynamic shared memory of a kernel, allowed once per kernel and device.
+template <auto Kernel>
+inline cudaError_t allow_smem(size_t bytes)
+{
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
 
 }  // namespace fp8
 
