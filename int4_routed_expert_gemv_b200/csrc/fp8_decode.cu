@@ -46,9 +46,9 @@ constexpr int kMaxPos = NT * 32;        // positions of the union lists: 16 toke
 constexpr uint32_t kSite = 60;
 
 struct Tables {
-    int expert[kMaxGroups], base[kMaxGroups], count[kMaxGroups];
+    Groups g;
     int pos[kMaxPos];                   // t * k + slot of each list position (-1: not of this batch)
-    float wt[kMaxPos];                  // its routing weight
+    float wt[kMaxPos];                  // routing weights [t * k + slot]
 };
 
 struct Smem {
@@ -119,11 +119,11 @@ struct Segments {
 __device__ __forceinline__ int row_of(const Params& p, const Tables& t, int g, int j)
 {
     if (j >= p.T) return -1;
-    if (t.expert[g] < 0) return t.base[g] + j;
+    if (t.g.expert[g] < 0) return t.g.base[g] + j;
     int r = -1;
-    for (int l = 0; l < t.count[g]; l++) {
-        const int a = t.pos[t.base[g] + l];
-        if (a >= 0 && a / p.k == j) r = t.base[g] + l;
+    for (int l = 0; l < t.g.count[g]; l++) {
+        const int a = t.pos[t.g.base[g] + l];
+        if (a >= 0 && a / p.k == j) r = t.g.base[g] + l;
     }
     return r;
 }
@@ -152,42 +152,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
         fence_barrier_init();
     }
     if (warp == 9) tmem_alloc(&sm.tmem, kTmem);
+    if (warp == 8 && lane < 3) prefetch_map(lane < 2 ? &p.w[lane] : &p.x[0]);
+    pdl_launch_dependents();
+    pdl_wait();
     if (warp == 8) {
-        if (lane < 2) prefetch_map(&p.w[lane]);
-        else if (lane == 2) prefetch_map(&p.x[0]);
-        // the groups: loads that do not wait for one another
-        int ng = 1;
-        if (MODE != FP8_DENSE) {
-            const int nu = *p.n_union;
-            for (int u = lane; u < p.E; u += 32) {
-                const int id = p.union_ids[u], b = p.offsets[u], e = p.offsets[u + 1];
-                const bool bad = id < 0 || id >= p.E || b < 0 || e < b || e > p.T * p.k;
-                const int g = p.n_shared + u;
-                sm.t.expert[g] = bad ? 0 : id;
-                sm.t.base[g] = bad ? 0 : b;
-                sm.t.count[g] = bad ? 0 : e - b;
-                if (bad && u < nu) set_flag(p.status, DEV_BAD_INDEX);
-                if (u >= nu) break;
-            }
-            if ((nu < 0 || nu > p.E) && lane == 0) set_flag(p.status, DEV_BAD_INDEX);
-            ng = p.n_shared + min(max(nu, 0), p.E);
-        }
-        if (lane == 0) {
-            if (MODE != FP8_DENSE && p.n_shared) {
-                sm.t.expert[0] = -1;
-                sm.t.base[0] = p.T * p.k;
-                sm.t.count[0] = p.T;
-            } else if (MODE == FP8_DENSE || ng == 0) {
-                // DOWN without any expert: one group that no column chose
-                sm.t.expert[0] = sm.t.base[0] = sm.t.count[0] = 0;
-            }
-            sm.n_groups = ng;
-        }
+        const int ng = read_groups<MODE>(p, lane, sm.t.g);
+        if (lane == 0) sm.n_groups = ng;
     } else if (MODE != FP8_DENSE && warp < 8) {
         for (int i = tid; i < p.T * p.k; i += kEpi) {
-            const int a = position_of(p, i);
-            sm.t.pos[i] = a;
-            if (MODE == FP8_DOWN) sm.t.wt[i] = a < 0 ? 0.0f : __ldg(p.wts + a);
+            sm.t.pos[i] = position_of(p, i);
+            if (MODE == FP8_DOWN) sm.t.wt[i] = __ldg(p.wts + i);
         }
     }
     tc_fence_before();
@@ -207,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
         while (sch.next(it)) {
             Segments<MODE> segs(p, it);
             while (segs.next(sg)) {
-                const int expert = sm.t.expert[sg.g];
+                const int expert = sm.t.g.expert[sg.g];
                 const CUtensorMap* wm = &p.w[expert < 0 ? 1 : 0];
                 const int z = max(expert, 0);
                 const int r0 = MODE == FP8_GATE_UP ? sg.rb * kM : sg.rb * 2 * kM;
@@ -285,9 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
         while (sch.next(it)) {
             Segments<MODE> segs(p, it);
             while (segs.next(sg)) {
-                const int expert = sm.t.expert[sg.g];
+                const int expert = sm.t.g.expert[sg.g];
                 const int row = MODE == FP8_DOWN ? row_of(p, sm.t, sg.g, j) : j < p.T ? j : -1;
-                const float wt = MODE != FP8_DOWN || expert < 0 || row < 0 ? 1.0f : sm.t.wt[row];
+                const float wt = MODE != FP8_DOWN || expert < 0 || row < 0 ? 1.0f : sm.t.wt[sm.t.pos[row]];
                 const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu;
                 const float* xs = p.xs + (size_t)max(row, 0) * p.kb;
                 const float* wb = expert < 0 ? p.ws[1]
@@ -382,28 +356,32 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 #pragma unroll
                     for (int j = 0; j < C; j++)
                         if (j < mine) __stcg(dst + (m * C + j) * kEpi, acc[m][j]);
-                __threadfence();
                 named_bar(1, kEpi);
-                if (tid == 0) {
-                    const uint32_t old = atomicAdd(&p.tickets[o0], 1u);
-                    const bool last = old == (uint32_t)(o1 - o0);
-                    if (last) p.tickets[o0] = 0;
-                    sm.last = last;
-                }
+                if (tid == 0) sm.last = arrive_last(&p.tickets[o0], (uint32_t)(o1 - o0 + 1));
                 named_bar(1, kEpi);
                 if (!sm.last) continue;
-                __threadfence();
 #pragma unroll
                 for (int m = 0; m < 2; m++)
 #pragma unroll
                     for (int j = 0; j < C; j++) acc[m][j] = 0.0f;
-                for (int o = o0; o <= o1; o++) {
-                    const float* src = p.partial + (size_t)(2 * o + (o == o0 ? 1 : 0)) * 2 * C * kEpi + tid;
+                // four parts' loads are under way together
+                for (int o = o0; o <= o1; o += 4) {
+                    float v[4][2][C];
 #pragma unroll
-                    for (int m = 0; m < 2; m++)
+                    for (int e = 0; e < 4; e++) {
+                        const float* src = p.partial + (size_t)(2 * (o + e) + (o + e == o0 ? 1 : 0)) * 2 * C * kEpi + tid;
 #pragma unroll
-                        for (int j = 0; j < C; j++)
-                            if (j < mine) acc[m][j] += __ldcg(src + (m * C + j) * kEpi);
+                        for (int m = 0; m < 2; m++)
+#pragma unroll
+                            for (int j = 0; j < C; j++)
+                                v[e][m][j] = j < mine && o + e <= o1 ? __ldcg(src + (m * C + j) * kEpi) : 0.0f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+#pragma unroll
+                        for (int m = 0; m < 2; m++)
+#pragma unroll
+                            for (int j = 0; j < C; j++) acc[m][j] += v[e][m][j];
                 }
             }
             if (MODE != FP8_GATE_UP) {
@@ -461,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
         // list positions that are none of the batch's
         if (MODE != FP8_DENSE && blockIdx.x == 0)
             for (int g = p.n_shared; g < ng; g++)
-                for (int l = tid; l < sm.t.count[g]; l += kEpi)
-                    if (sm.t.pos[sm.t.base[g] + l] < 0) set_flag(p.status, DEV_BAD_INDEX);
+                for (int l = tid; l < sm.t.g.count[g]; l += kEpi)
+                    if (sm.t.pos[sm.t.g.base[g] + l] < 0) set_flag(p.status, DEV_BAD_INDEX);
     }
     tc_fence_before();
     __syncthreads();
@@ -477,8 +455,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t s)
 {
     const cudaError_t e = allow_smem<fp8_decode_kernel<MODE>>(kSmem);
     if (e != cudaSuccess) return e;
-    fp8_decode_kernel<MODE><<<grid, kThreads, kSmem, s>>>(p);
-    return cudaGetLastError();
+    return launch_early<fp8_decode_kernel<MODE>>(grid, kThreads, kSmem, s, p);
 }
 
 }  // namespace

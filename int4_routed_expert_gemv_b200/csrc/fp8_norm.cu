@@ -14,10 +14,12 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
-#include "fp8.cuh"
+#include "fp8_tiles.cuh"
 
 namespace coli {
 namespace {
+
+using fp8::bf16x2_bits;
 
 struct Row8 {
     float v[8];
@@ -42,12 +44,6 @@ __device__ __forceinline__ Row8 load8(const void* base, size_t elem)
         r.v[4] = b.x; r.v[5] = b.y; r.v[6] = b.z; r.v[7] = b.w;
     }
     return r;
-}
-
-__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
-{
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&b);
 }
 
 template <bool BF16>

@@ -52,7 +52,7 @@ constexpr int kJoin = 12;                         // what joining the parts of a
 constexpr int kPitch = 144;                       // bytes of a staged row: 128 and a gap
 constexpr size_t kOut = (size_t)kEpi * kPitch;
 constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 2 * kM * 4 +
-                         (kMaxGroups + 3) / 4 * 4 * 4 + 16 + 256;
+                         (kMaxGroups + 3) / 4 * 4 * 4 + sizeof(Groups) + 16 + 16 + 256;
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -255,7 +255,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* out_stage = smem + kStages * (size_t)kStage;
     uint32_t* tops = reinterpret_cast<uint32_t*>(out_stage + kOut);          // [2][kM] maxima of the SwiGLU rows
     int* first = reinterpret_cast<int*>(tops + 2 * kM);
-    int* flags = first + (kMaxGroups + 3) / 4 * 4;         // [0] groups [1] tiles [2] last part [3] tensor memory
+    Groups& groups = *reinterpret_cast<Groups*>(first + (kMaxGroups + 3) / 4 * 4);
+    // [0] groups [1] tiles [2] last part [3] tensor memory
+    int* flags = reinterpret_cast<int*>((reinterpret_cast<uintptr_t>(&groups + 1) + 15) & ~uintptr_t(15));
     uint64_t* bars = reinterpret_cast<uint64_t*>(flags + 4);
     uint64_t* full = bars;                       // [kStages] rank 0: both CTAs' tiles landed
     uint64_t* empty = full + kStages;            // [kStages] MMAs done with the stage
@@ -284,7 +286,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    if (warp == 8) plan_tiles<MODE>(p, NT, lane, first, &flags[0], &flags[1]);
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == 8) {
+        const int ng = read_groups<MODE>(p, lane, groups);
+        const int tiles = plan_tiles(p, groups, ng, NT, lane, first);
+        if (lane == 0) {
+            flags[0] = ng;
+            flags[1] = tiles;
+        }
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -297,12 +308,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Item it;
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 8) {
             // ----------------------------- TMA producer ---------------------------------
             uint32_t n = 0;
             while (sch.next(it)) {
-                const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
+                const Tile tl = tile_of(p, groups, first, n_groups, NT, it.tile);
                 const int shared = tl.g.expert < 0 ? 1 : 0;
                 const CUtensorMap* wm = &p.w[shared];
                 const CUtensorMap* xm = &p.x[MODE == FP8_GATE_UP ? shared : 0];
@@ -369,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------- scaled accumulation, outputs -------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int wg = warp >> 2, q = warp & 3;     // warpgroup, tensor memory lane quarter
         const int row = q * 32 + lane;              // token within the CTA's 128
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
@@ -378,29 +389,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t n = 0;
         const uint32_t ae = map_to(&acc_empty[0], 0);
         const int nb = fp8_blocks(p.rows);
-        while (sch.next(it)) {
-            const Tile tl = tile_of<MODE>(p, first, n_groups, NT, it.tile);
-            const int left = tl.n - rank * kM - q * 32;         // tokens of this warp
+        // What a tile needs besides its sums.  The next tile's is looked up (list positions, then
+        // scales: loads that wait for one another) before this one's outputs are written.
+        struct Work {
+            Item it;
+            int rb, expert, left;        // row block, expert, tokens of this warp
+            int xrow, orow;              // row of the token's scales, row of y / h / z (-1: none)
+        };
+        float xn[4], an[4], bn[4];       // scales of the next four K steps: token, both row blocks
+        auto fetch = [&](const Work& w, int kb) {
+            const float* xs = p.xs + (size_t)w.xrow * p.kb;
+            const float* wa = w.expert < 0 ? p.ws[1]
+                                           : reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws[0]) +
+                                                                            (uint64_t)w.expert * p.ws_stride);
+            wa += (size_t)(MODE == FP8_GATE_UP ? w.rb : 2 * w.rb) * p.kb;
+            const float* wb = MODE == FP8_GATE_UP ? wa + (size_t)nb * p.kb : 2 * w.rb + 1 < nb ? wa + p.kb : wa;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int k = min(kb + i, w.it.kb1 - 1);
+                xn[i] = __ldg(xs + k);
+                an[i] = __ldg(wa + k);
+                bn[i] = __ldg(wb + k);
+            }
+        };
+        auto look_up = [&](Work& w) {
+            if (!sch.next(w.it)) return false;
+            const Tile tl = tile_of(p, groups, first, n_groups, NT, w.it.tile);
+            w.rb = tl.rb;
+            w.expert = tl.g.expert;
+            w.left = tl.n - rank * kM - q * 32;
             const int tok = tl.t0 + rank * kM + row;            // token of the group
-            const bool valid = lane < left;
-            // row of x, and where the outputs go: row of y / h, or of z (-1: nowhere)
-            int xrow = MODE == FP8_DENSE || tl.g.expert < 0 ? tok : 0, orow = valid ? tok : -1;
-            if (MODE != FP8_DENSE && valid) {
-                const int a = tl.g.expert < 0 ? 0 : position_of(p, tl.g.base + tok);
-                if (MODE == FP8_DOWN) {
-                    xrow = tl.g.base + tok;
-                    orow = tl.g.expert < 0 ? xrow : a;
-                    if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                    else if (tl.g.expert >= 0 && tl.rb == 0 && wg == 0) p.present[a] = 1;
+            w.xrow = 0;
+            w.orow = -1;
+            if (lane < w.left) {
+                if (MODE == FP8_DENSE) {
+                    w.xrow = w.orow = tok;
+                } else if (tl.g.expert < 0) {
+                    w.xrow = MODE == FP8_DOWN ? tl.g.base + tok : tok;
+                    w.orow = tl.g.base + tok;
                 } else {
-                    if (tl.g.expert >= 0) xrow = max(a, 0) / p.k;
-                    orow = a < 0 ? -1 : tl.g.base + tok;
+                    const int a = position_of(p, tl.g.base + tok);
+                    w.xrow = MODE == FP8_DOWN ? tl.g.base + tok : max(a, 0) / p.k;
+                    if (a >= 0) w.orow = MODE == FP8_DOWN ? a : tl.g.base + tok;
+                    if (MODE == FP8_DOWN) {
+                        if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
+                        else if (tl.rb == 0 && wg == 0) p.present[a] = 1;
+                    }
                 }
             }
-            if (MODE == FP8_DENSE && p.residual && orow >= 0 && it.kb1 == p.kb) {
+            if (MODE == FP8_DENSE && p.residual && w.orow >= 0 && w.it.kb1 == p.kb) {
                 // the thread's part of the residual's row into L2
                 const int es = p.y_bf16 ? 2 : 4;
-                const uint8_t* r = reinterpret_cast<const uint8_t*>(p.residual) + (size_t)orow * p.rows * es;
+                const uint8_t* r = reinterpret_cast<const uint8_t*>(p.residual) + (size_t)w.orow * p.rows * es;
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int c = (2 * tl.rb + h) * kM + wg * 64;
@@ -408,28 +448,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (c + o / es < p.rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + (size_t)c * es + o));
                 }
             }
-            const float* xs = p.xs + (size_t)(valid ? xrow : 0) * p.kb;
-            const float* wbase = tl.g.expert < 0
-                                     ? p.ws[1]
-                                     : reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws[0]) +
-                                                                      (uint64_t)tl.g.expert * p.ws_stride);
-            const float* wa = wbase + (size_t)(MODE == FP8_GATE_UP ? tl.rb : 2 * tl.rb) * p.kb;
-            const float* wb = MODE == FP8_GATE_UP ? wa + (size_t)nb * p.kb : 2 * tl.rb + 1 < nb ? wa + p.kb : wa;
+            if (w.left > 0) fetch(w, w.it.kb0);
+            return true;
+        };
+        // (DENSE has no lists, and the registers are dear: there it is looked up when due.)
+        constexpr bool kAhead = MODE != FP8_DENSE;
+        Work next;
+        bool more = kAhead ? look_up(next) : true;
+        while (more) {
+            if (!kAhead && !look_up(next)) break;
+            const Work w = next;
+            const int left = w.left;
+            it = w.it;
 #pragma unroll
             for (int j = 0; j < C; j++) acc[j] = 0.0f;
             if (left > 0) {
                 // scales of four K steps at a time, fetched four steps ahead
-                float xn[4], an[4], bn[4];
-                auto fetch = [&](int kb) {
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int k = min(kb + i, it.kb1 - 1);
-                        xn[i] = __ldg(xs + k);
-                        an[i] = __ldg(wa + k);
-                        bn[i] = __ldg(wb + k);
-                    }
-                };
-                fetch(it.kb0);
                 for (int kb = it.kb0; kb < it.kb1; kb += 4) {
                     float sa[4], sb[4];
 #pragma unroll
@@ -437,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         sa[i] = xn[i] * an[i];
                         sb[i] = xn[i] * bn[i];
                     }
-                    if (kb + 4 < it.kb1) fetch(kb + 4);
+                    if (kb + 4 < it.kb1) fetch(w, kb + 4);
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         if (kb + i >= it.kb1) break;
@@ -471,6 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (lane == 0) arrive_pair(ae + b * 8);
                 }
             }
+            if (kAhead) more = look_up(next);
             if (it.kb1 - it.kb0 < p.kb) {
                 // store the sums; the last part to arrive adds all of them up
                 const int o0 = sch.owner(it.tile * p.kb), o1 = sch.owner(it.tile * p.kb + p.kb - 1);
@@ -482,17 +517,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         __stcg(dst + j * kEpi, make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
                     }
                 }
-                __threadfence();
                 named_bar(1, kEpi);
-                if (tid == 0) {
-                    uint32_t* t = &p.tickets[2 * o0 + rank];
-                    const bool last = atomicAdd(t, 1u) == (uint32_t)(o1 - o0);
-                    if (last) *t = 0;
-                    flags[2] = last;
-                }
+                if (tid == 0) flags[2] = arrive_last(&p.tickets[2 * o0 + rank], (uint32_t)(o1 - o0 + 1));
                 named_bar(1, kEpi);
                 if (!flags[2]) continue;
-                __threadfence();
                 if (left > 0) {
 #pragma unroll
                     for (int j = 0; j < C; j++) acc[j] = 0.0f;
@@ -513,19 +541,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (MODE != FP8_GATE_UP) {
                 if (left <= 0) continue;
                 // output columns of the thread's two runs of 64
-                const int c0 = 2 * tl.rb * kM + wg * 64;
-                if (MODE == FP8_DOWN) store_rows<float>(p.z, nullptr, p.rows, c0, orow, acc, stage, lane);
+                const int c0 = 2 * w.rb * kM + wg * 64;
+                if (MODE == FP8_DOWN) store_rows<float>(p.z, nullptr, p.rows, c0, w.orow, acc, stage, lane);
                 else if (p.y_bf16)
                     store_rows<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.y),
-                                              reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, orow, acc,
+                                              reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.orow, acc,
                                               stage, lane);
                 else
                     store_rows<float>(reinterpret_cast<float*>(p.y), reinterpret_cast<const float*>(p.residual), p.rows, c0,
-                                      orow, acc, stage, lane);
+                                      w.orow, acc, stage, lane);
             } else {
                 // SwiGLU of 64 columns; the scale block is this and the other warpgroup's
                 uint32_t top = 0;
-                if (left > 0 && tl.rb * kM + wg * 64 < p.I) {            // I is a multiple of 64
+                if (left > 0 && w.rb * kM + wg * 64 < p.I) {            // I is a multiple of 64
 #pragma unroll
                     for (int j = 0; j < 64; j++) {
                         acc[j] = swiglu(acc[j], acc[64 + j]);
@@ -537,9 +565,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 top = max(top, tops[(wg ^ 1) * kM + row]);
                 named_bar(1, kEpi);      // read before the next tile's
                 const Quantizer qz(top);
-                const int i0 = tl.rb * kM + wg * 64;
-                if (orow >= 0 && i0 < p.I) {
-                    uint4* to = reinterpret_cast<uint4*>(p.hq + (size_t)orow * p.I + i0);
+                const int i0 = w.rb * kM + wg * 64;
+                if (w.orow >= 0 && i0 < p.I) {
+                    uint4* to = reinterpret_cast<uint4*>(p.hq + (size_t)w.orow * p.I + i0);
 #pragma unroll
                     for (int j = 0; j < 64; j += 16) {
                         uint32_t w[4];
@@ -550,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         to[j / 16] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    if (wg == 0) p.hs[(size_t)orow * nb + tl.rb] = qz.scale;
+                    if (wg == 0) p.hs[(size_t)w.orow * nb + w.rb] = qz.scale;
                 }
             }
         }
@@ -569,8 +597,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t s)
 {
     const cudaError_t e = allow_smem<fp8_pair_kernel<MODE>>(kSmem);
     if (e != cudaSuccess) return e;
-    fp8_pair_kernel<MODE><<<grid, kThreads, kSmem, s>>>(p);
-    return cudaGetLastError();
+    return launch_early<fp8_pair_kernel<MODE>>(grid, kThreads, kSmem, s, p);
 }
 
 }  // namespace

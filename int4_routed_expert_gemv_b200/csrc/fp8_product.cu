@@ -23,6 +23,8 @@ __global__ void __launch_bounds__(256) fp8_combine_kernel(int T, int k, int H, i
                                                           const uint8_t* present, const float* w,
                                                           const float* residual, float* y)
 {
+    pdl_launch_dependents();
+    pdl_wait();
     const int h4 = H / 4;
     const int64_t total = (int64_t)T * h4;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
@@ -50,12 +52,22 @@ __global__ void __launch_bounds__(256) fp8_combine_kernel(int T, int k, int H, i
     }
 }
 
+__global__ void __launch_bounds__(256) fp8_clear_kernel(size_t n, uint4* p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) p[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Rows of x in list order: row p is token assign[p] / k.  Positions that are none of the
 // batch's are flagged and leave their row as it is.
 __global__ void __launch_bounds__(256) fp8_gather_kernel(int positions, int k, int E, int pieces, const int32_t* n_union,
                                                          const int32_t* offsets, const int32_t* assign, const uint4* x,
                                                          uint4* to, uint32_t* status)
 {
+    pdl_launch_dependents();
+    pdl_wait();
     const int nu = min(max(*n_union, 0), E);
     const int64_t total = (int64_t)min(max(offsets[nu], 0), positions) * pieces;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
@@ -178,10 +190,9 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     if (a.mode == FP8_GATE_UP && !decode) {
         const int64_t pieces = (int64_t)a.T * a.k * (a.H / 16);
         const int blocks = (int)(pieces + 255 < (int64_t)256 * a.num_sms * 8 ? (pieces + 255) / 256 : (int64_t)a.num_sms * 8);
-        fp8_gather_kernel<<<blocks, 256, 0, s>>>(a.T * a.k, a.k, a.E, a.H / 16, a.n_union, a.offsets, a.assign,
-                                                 reinterpret_cast<const uint4*>(a.x), reinterpret_cast<uint4*>(gathered),
-                                                 a.status);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_early<fp8_gather_kernel>(blocks, 256, 0, s, a.T * a.k, a.k, a.E, a.H / 16, a.n_union,
+                                                              a.offsets, a.assign, reinterpret_cast<const uint4*>(a.x),
+                                                              reinterpret_cast<uint4*>(gathered), a.status);
         if (e != cudaSuccess) return e;
     }
     p.wts = a.wts;
@@ -189,15 +200,17 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     uint8_t* at = a.scratch + partial_bytes(a.T);
     p.present = at;
     p.z = reinterpret_cast<float*>(at + up((size_t)a.T * a.k));
-    cudaError_t e = cudaMemsetAsync(p.present, 0, (size_t)a.T * a.k, s);
+    const size_t words = up((size_t)a.T * a.k) / 16;
+    cudaError_t e = launch_early<fp8_clear_kernel>((int)((words + 255) / 256), 256, 0, s, words,
+                                                   reinterpret_cast<uint4*>(p.present));
     if (e != cudaSuccess) return e;
     e = product();
     if (e != cudaSuccess) return e;
     const int64_t work = (int64_t)a.T * (a.H / 4);
     const int blocks = (int)(work + 255 < (int64_t)256 * a.num_sms * 8 ? (work + 255) / 256 : (int64_t)a.num_sms * 8);
-    fp8_combine_kernel<<<blocks, 256, 0, s>>>(a.T, a.k, a.H, a.n_shared, p.z, p.present, a.wts,
-                                              reinterpret_cast<const float*>(a.residual), reinterpret_cast<float*>(a.y));
-    return cudaGetLastError();
+    return launch_early<fp8_combine_kernel>(blocks, 256, 0, s, a.T, a.k, a.H, a.n_shared, (const float*)p.z,
+                                            (const uint8_t*)p.present, a.wts, reinterpret_cast<const float*>(a.residual),
+                                            reinterpret_cast<float*>(a.y));
 }
 
 }  // namespace coli

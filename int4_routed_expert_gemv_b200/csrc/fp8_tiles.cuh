@@ -67,37 +67,52 @@ __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8])
                  : "r"(a));
 }
 
-// Group g of a product: the shared expert first (the longest), then the union.
+// A group of tokens: all of them (DENSE), the shared expert's, or those of one expert of the
+// union.  The shared expert, the longest, comes first.
 struct Group {
     int expert;   // -1: shared
     int base;     // first row (position in the union lists; T*k + t for the shared expert)
     int count;    // 0 where the lists are not a batch union's: nothing of them is read or written
-    bool bad;
 };
 
+struct Groups {
+    int expert[kMaxGroups], base[kMaxGroups], count[kMaxGroups];
+    __device__ __forceinline__ Group at(int g) const { return Group{expert[g], base[g], count[g]}; }
+};
+
+// One warp: the groups of a launch into shared memory (loads that do not wait for one
+// another); returns how many there are.
 template <int MODE>
-__device__ __forceinline__ Group group_of(const Params& p, int g)
+__device__ __forceinline__ int read_groups(const Params& p, int lane, Groups& t)
 {
-    Group v;
-    v.bad = false;
-    if (MODE == FP8_DENSE) {
-        v.expert = 0;
-        v.base = 0;
-        v.count = p.T;
-    } else if (g < p.n_shared) {
-        v.expert = -1;
-        v.base = p.T * p.k;
-        v.count = p.T;
-    } else {
-        const int u = g - p.n_shared;
-        v.expert = p.union_ids[u];
-        v.base = p.offsets[u];
-        const int end = p.offsets[u + 1];
-        v.bad = v.expert < 0 || v.expert >= p.E || v.base < 0 || end < v.base || end > p.T * p.k;
-        v.count = v.bad ? 0 : end - v.base;
-        if (v.bad) v.expert = v.base = 0;
+    int ng = 1;
+    if (MODE != FP8_DENSE) {
+        const int nu = *p.n_union;
+        for (int u = lane; u < p.E; u += 32) {
+            const int id = p.union_ids[u], b = p.offsets[u], e = p.offsets[u + 1];
+            const bool bad = id < 0 || id >= p.E || b < 0 || e < b || e > p.T * p.k;
+            const int g = p.n_shared + u;
+            t.expert[g] = bad ? 0 : id;
+            t.base[g] = bad ? 0 : b;
+            t.count[g] = bad ? 0 : e - b;
+            if (u >= nu) break;
+            if (bad) set_flag(p.status, DEV_BAD_INDEX);
+        }
+        if ((nu < 0 || nu > p.E) && lane == 0) set_flag(p.status, DEV_BAD_INDEX);
+        ng = p.n_shared + min(max(nu, 0), p.E);
     }
-    return v;
+    if (lane == 0) {
+        if (MODE != FP8_DENSE && p.n_shared) {
+            t.expert[0] = -1;
+            t.base[0] = p.T * p.k;
+            t.count[0] = p.T;
+        } else if (MODE == FP8_DENSE || ng == 0) {
+            t.expert[0] = t.base[0] = 0;
+            t.count[0] = MODE == FP8_DENSE ? p.T : 0;
+        }
+    }
+    __syncwarp();
+    return ng;
 }
 
 // Token of row `pos` of the union lists (-1: not a position of this batch).
@@ -172,8 +187,7 @@ struct Tile {
 };
 
 // first[g]: tiles of nt tokens before group g.
-template <int MODE>
-__device__ __forceinline__ Tile tile_of(const Params& p, const int* first, int n_groups, int nt, int tile)
+__device__ __forceinline__ Tile tile_of(const Params& p, const Groups& t, const int* first, int n_groups, int nt, int tile)
 {
     Tile v;
     const int q = tile / p.rb;
@@ -184,31 +198,19 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const int* first, int n
         if (first[mid] <= q) lo = mid;
         else hi = mid;
     }
-    v.g = group_of<MODE>(p, lo);
+    v.g = t.at(lo);
     v.t0 = (q - first[lo]) * nt;
     v.n = min(nt, v.g.count - v.t0);
     return v;
 }
 
-// One warp: first[] of every group, the groups and the tiles.
-template <int MODE>
-__device__ __forceinline__ void plan_tiles(const Params& p, int nt, int lane, int* first, int* n_groups, int* tiles)
+// One warp: first[] of every group; returns the tiles.
+__device__ __forceinline__ int plan_tiles(const Params& p, const Groups& t, int ng, int nt, int lane, int* first)
 {
-    int ng = 1;
-    if (MODE != FP8_DENSE) {
-        const int nu = *p.n_union;
-        if ((nu < 0 || nu > p.E) && lane == 0) set_flag(p.status, DEV_BAD_INDEX);
-        ng = p.n_shared + min(max(nu, 0), p.E);
-    }
     int base = 0;
     for (int g0 = 0; g0 < ng; g0 += 32) {
         const int g = g0 + lane;
-        int n = 0;
-        if (g < ng) {
-            const Group v = group_of<MODE>(p, g);
-            if (v.bad) set_flag(p.status, DEV_BAD_INDEX);
-            n = (v.count + nt - 1) / nt;
-        }
+        const int n = g < ng ? (t.count[g] + nt - 1) / nt : 0;
         int x = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -218,10 +220,7 @@ __device__ __forceinline__ void plan_tiles(const Params& p, int nt, int lane, in
         if (g < ng) first[g] = base + x - n;
         base += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) {
-        *n_groups = ng;
-        *tiles = base * p.rb;
-    }
+    return base * p.rb;
 }
 
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
@@ -233,6 +232,17 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
 // silu(g) * u: expf and the quotient are within 2 ulp each; the quotient's 0 for 1 + exp(-g)
 // above 2^126 is off by less than the smallest normal number.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+
+// One thread, after its CTA's barrier: counts a part of a tile whose sums the CTA has stored.
+// True for the last of `parts`, which then sees the others' sums; the counter is 0 again.
+__device__ __forceinline__ bool arrive_last(uint32_t* ticket, uint32_t parts)
+{
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+    const bool last = old == parts - 1;
+    if (last) *ticket = 0;
+    return last;
+}
 
 // Dynamic shared memory of a kernel, allowed once per kernel and device.
 template <auto Kernel>
@@ -246,6 +256,24 @@ inline cudaError_t allow_smem(size_t bytes)
     e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     return e;
+}
+
+// Launch that may begin while the kernel before it in the stream ends: its set-up then costs
+// no time of its own.  Kernels launched so wait (pdl_wait) before they touch memory.
+template <auto Kernel, class... A>
+inline cudaError_t launch_early(int grid, int threads, size_t smem, cudaStream_t s, const A&... args)
+{
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = a;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, Kernel, args...);
 }
 
 }  // namespace fp8
