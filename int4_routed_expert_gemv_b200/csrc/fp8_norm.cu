@@ -147,12 +147,14 @@ __global__ void __launch_bounds__(STEPS == 4 ? 1024 : 768) fp8_norm_kernel(Fp8No
 }
 
 template <bool BF16>
-cudaError_t launch(const Fp8NormParams& p, cudaStream_t s)
+cudaError_t launch(const Fp8NormParams& p, int num_sms, cudaStream_t s)
 {
     const int chunks = (p.H + 7) / 8;                 // 8-column pieces of a row
-    // up to 768 threads a row and one piece each; longer rows take more pieces a thread
+    // With few rows a piece a thread, for the shortest way through a row; with many, four, so
+    // that more rows are on an SM and one's loads run beside another's reduction.
     auto threads = [&](int steps) { return ((chunks + steps - 1) / steps + 31) / 32 * 32; };
-    if (chunks <= 768) fp8_norm_kernel<BF16, 1><<<p.T, threads(1), 0, s>>>(p);
+    if (p.T > 2 * num_sms && chunks >= 128) fp8_norm_kernel<BF16, 4><<<p.T, threads(4), 0, s>>>(p);
+    else if (chunks <= 768) fp8_norm_kernel<BF16, 1><<<p.T, threads(1), 0, s>>>(p);
     else if (chunks <= 1536) fp8_norm_kernel<BF16, 2><<<p.T, threads(2), 0, s>>>(p);
     else fp8_norm_kernel<BF16, 4><<<p.T, threads(4), 0, s>>>(p);
     return cudaGetLastError();
@@ -162,8 +164,7 @@ cudaError_t launch(const Fp8NormParams& p, cudaStream_t s)
 
 cudaError_t fp8_norm_launch(const Fp8NormParams& p, int num_sms, cudaStream_t s)
 {
-    (void)num_sms;
-    return p.bf16 ? launch<true>(p, s) : launch<false>(p, s);
+    return p.bf16 ? launch<true>(p, num_sms, s) : launch<false>(p, num_sms, s);
 }
 
 }  // namespace coli

@@ -303,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = (uint32_t)flags[3];
     const int n_groups = flags[0];
     Schedule sch;
-    sch.init(flags[1], p.kb, (int)n_clusters(), (int)cluster_id(), kLeast, kJoin);
+    sch.init(flags[1], p.kb, (int)n_clusters(), (int)cluster_id(), kLeast, kJoin, p.slices);
     bool dead = false;
     Item it;
 
@@ -437,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (MODE == FP8_DENSE && p.residual && w.orow >= 0 && w.it.kb1 == p.kb) {
+            if (MODE == FP8_DENSE && p.residual && p.slices == 1 && w.orow >= 0 && w.it.kb1 == p.kb) {
                 // the thread's part of the residual's row into L2
                 const int es = p.y_bf16 ? 2 : 4;
                 const uint8_t* r = reinterpret_cast<const uint8_t*>(p.residual) + (size_t)w.orow * p.rows * es;
@@ -506,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             if (kAhead) more = look_up(next);
-            if (it.kb1 - it.kb0 < p.kb) {
+            if (it.kb1 - it.kb0 < p.kb && p.slices == 1) {
                 // store the sums; the last part to arrive adds all of them up
                 const int o0 = sch.owner(it.tile * p.kb), o1 = sch.owner(it.tile * p.kb + p.kb - 1);
                 float4* dst = reinterpret_cast<float4*>(p.partial) +
@@ -543,6 +543,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // output columns of the thread's two runs of 64
                 const int c0 = 2 * w.rb * kM + wg * 64;
                 if (MODE == FP8_DOWN) store_rows<float>(p.z, nullptr, p.rows, c0, w.orow, acc, stage, lane);
+                else if (p.slices > 1)
+                    store_rows<float>(p.partial + (size_t)it.slice * p.T * p.pitch, nullptr, p.pitch, c0, w.orow, acc, stage,
+                                      lane);
                 else if (p.y_bf16)
                     store_rows<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.y),
                                               reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.orow, acc,

@@ -17,6 +17,33 @@ namespace {
 
 using namespace fp8;
 
+// y = residual + the slices' sums, in K order.  One thread 4 columns of a row.
+template <class Y>
+__global__ void __launch_bounds__(256) fp8_join_kernel(int T, int N, int pitch, int slices, const float* part,
+                                                       const Y* residual, Y* y)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int n4 = pitch / 4;
+    const int64_t total = (int64_t)T * n4;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int t = (int)(i / n4), c = (int)(i - (int64_t)t * n4) * 4;
+        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int s = 0; s < slices; s++) {
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(part) + (size_t)s * total + i);
+            f[0] += a.x;
+            f[1] += a.y;
+            f[2] += a.z;
+            f[3] += a.w;
+        }
+        const size_t o = (size_t)t * N + c;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (c + e < N) y[o + e] = (Y)(f[e] + (residual ? (float)residual[o + e] : 0.0f));
+    }
+}
+
 // y[t] = residual[t] + z[T*k + t] (shared) + sum over slots of w[t][s] * z[t*k + s], in slot
 // order; slots that the lists leave out add nothing.
 __global__ void __launch_bounds__(256) fp8_combine_kernel(int T, int k, int H, int n_shared, const float* z,
@@ -184,6 +211,19 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     p.status = a.status;
     p.tickets = a.tickets;
     p.partial = reinterpret_cast<float*>(a.scratch);
+    p.slices = 1;
+    if (a.mode == FP8_DENSE && !decode) {
+        // Fewer tiles than half of the pairs: equal slices of K, at least 4 K steps each, and a
+        // second launch that adds them up on every SM.  (Joining parts as the last one arrives
+        // leaves that to one pair per tile: 77 x 576 x 6144 took 24 us so.)
+        const int pairs = (a.num_sms < kFp8Ctas ? a.num_sms : kFp8Ctas) / 2;
+        const int64_t tiles = (int64_t)((a.T + 255) / 256) * p.rb;
+        if (2 * tiles <= pairs) {
+            const int most = p.kb / 4, fit = pairs / (int)tiles;
+            p.slices = most < 2 ? 1 : most < fit ? most : fit;
+        }
+        p.pitch = (a.N + 3) / 4 * 4;
+    }
     auto product = [&]() {
         return decode ? fp8_decode_launch(a.mode, p, a.num_sms, s) : fp8_pair_launch(a.mode, p, a.num_sms, s);
     };
@@ -196,6 +236,19 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
         if (e != cudaSuccess) return e;
     }
     p.wts = a.wts;
+    if (p.slices > 1) {
+        const cudaError_t e = product();
+        if (e != cudaSuccess) return e;
+        const int64_t work = (int64_t)a.T * (p.pitch / 4);
+        const int blocks = (int)(work + 255 < (int64_t)256 * a.num_sms * 8 ? (work + 255) / 256 : (int64_t)a.num_sms * 8);
+        const float* part = p.partial;
+        if (a.y_bf16)
+            return launch_early<fp8_join_kernel<__nv_bfloat16>>(blocks, 256, 0, s, a.T, a.N, p.pitch, p.slices, part,
+                                                                reinterpret_cast<const __nv_bfloat16*>(a.residual),
+                                                                reinterpret_cast<__nv_bfloat16*>(a.y));
+        return launch_early<fp8_join_kernel<float>>(blocks, 256, 0, s, a.T, a.N, p.pitch, p.slices, part,
+                                                    reinterpret_cast<const float*>(a.residual), reinterpret_cast<float*>(a.y));
+    }
     if (a.mode != FP8_DOWN || decode) return product();
     uint8_t* at = a.scratch + partial_bytes(a.T);
     p.present = at;

@@ -38,7 +38,8 @@ struct Params {
     float* hs;
     float* z;                     // DOWN: [T*k + T*n_shared][rows]
     uint8_t* present;             // DOWN: [T*k] 1 where z has the row
-    float* partial;               // sums of the parts of split tiles
+    float* partial;               // sums of the parts of split tiles, or slices [slices][T][pitch]
+    int slices, pitch;
     uint32_t* tickets;            // parts that have arrived, by the first part's worker
     uint32_t* status;
 };
@@ -123,21 +124,24 @@ __device__ __forceinline__ int position_of(const Params& p, int pos)
 }
 
 struct Item {
-    int tile, kb0, kb1;
+    int tile, kb0, kb1, slice;
 };
 
 // The items of worker c of G (a CTA or a pair): a run of K steps over the first `split` tiles,
 // then whole tiles.  `least`: K steps of a run at least, so that the parts of a tile, which
 // one worker adds up, stay few.
+// Or, with slices > 1, every tile in so many equal runs of K steps, whose sums another launch
+// adds up.
 struct Schedule {
-    int tiles, split, kb, G, c;
+    int tiles, split, kb, G, c, slices;
     int per, more, n_run;         // units per run, runs with one more, runs
     int u, u1, t;
 
     // join: what joining the parts of a tile costs, in K steps.  Splitting has to save more;
     // a worker alone streams a quarter faster than all of them together.
-    __device__ void init(int tiles_, int kb_, int G_, int c_, int least, int join)
+    __device__ void init(int tiles_, int kb_, int G_, int c_, int least, int join, int slices_ = 1)
     {
+        slices = slices_;
         tiles = tiles_;
         kb = kb_;
         G = G_;
@@ -145,7 +149,7 @@ struct Schedule {
         const int rest = tiles % G;
         const int waves = (tiles + G - 1) / G;
         const int whole = waves == 1 ? kb * max(tiles, 4 * G / 5) / G : waves * kb;
-        split = rest == 0 || whole <= (int)((int64_t)tiles * kb / G) + join ? 0 : tiles < G ? tiles : rest + G;
+        split = slices > 1 || rest == 0 || whole <= (int)((int64_t)tiles * kb / G) + join ? 0 : tiles < G ? tiles : rest + G;
         const int units = split * kb;
         n_run = min(G, max(1, units / least));
         per = units / n_run;
@@ -166,13 +170,15 @@ struct Schedule {
             it.tile = u / kb;
             it.kb0 = u - it.tile * kb;
             it.kb1 = min(kb, it.kb0 + u1 - u);
+            it.slice = 0;
             u += it.kb1 - it.kb0;
             return true;
         }
-        if (t < tiles) {
-            it.tile = t;
-            it.kb0 = 0;
-            it.kb1 = kb;
+        if (t < tiles * slices) {
+            it.tile = t / slices;
+            it.slice = t - it.tile * slices;
+            it.kb0 = (int)((int64_t)kb * it.slice / slices);
+            it.kb1 = (int)((int64_t)kb * (it.slice + 1) / slices);
             t += G;
             return true;
         }
