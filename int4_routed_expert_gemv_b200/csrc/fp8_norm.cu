@@ -2,15 +2,16 @@
 // columns, in one pass over the row.
 //
 //   sum = x + residual (one rounding to the stream's type; the norm sees the rounded sum),
-//   n   = float(sum * gamma / sqrt(mean(sum^2) + eps))   (sum of squares and scaling in
-//         double and rounded once, like coli_rmsnorm: n feeds the router, whose top-k is
+//   n   = float(sum * gamma / sqrt(mean(sum^2) + eps))   (sum of squares and root in double
+//         and one rounding at the end, like coli_rmsnorm: n feeds the router, whose top-k is
 //         decided on floats),
 //   scale[b] = max |n| of the block / 448,  q = e4m3(n / scale) (fp32 quotient, to nearest
 //         even; 0 where the scale is 0).
 //
 // Memory-bound: a row is read once into registers (8 consecutive columns a thread and step),
 // reduced across the CTA, and written out as sum, n, codes and scales.  16 neighbouring lanes
-// hold one scale block, so its maximum is four shuffles.
+// hold one scale block, so its maximum is four shuffles.  The scaling is done in pairs of
+// floats rather than doubles, whose conversions (16 a cycle and SM) cost more than the loads.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -25,82 +26,102 @@ struct Row8 {
     float v[8];
 };
 
+// 8 columns as they are kept: fp32, or bf16 pairs.
 template <bool BF16>
-__device__ __forceinline__ Row8 load8(const void* base, size_t elem)
-{
-    Row8 r;
-    if (BF16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + elem);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            r.v[2 * j] = __uint_as_float(w[j] << 16);
-            r.v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-    } else {
-        const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + elem);
-        const float4 a = f[0], b = f[1];
-        r.v[0] = a.x; r.v[1] = a.y; r.v[2] = a.z; r.v[3] = a.w;
-        r.v[4] = b.x; r.v[5] = b.y; r.v[6] = b.z; r.v[7] = b.w;
-    }
-    return r;
-}
+struct Piece {
+    uint32_t w[BF16 ? 4 : 8];
 
-template <bool BF16>
-__device__ __forceinline__ void store8(void* base, size_t elem, const Row8& r)
-{
-    if (BF16) {
-        uint4 u;
-        u.x = bf16x2_bits(r.v[0], r.v[1]);
-        u.y = bf16x2_bits(r.v[2], r.v[3]);
-        u.z = bf16x2_bits(r.v[4], r.v[5]);
-        u.w = bf16x2_bits(r.v[6], r.v[7]);
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + elem) = u;
-    } else {
-        float4* f = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + elem);
-        f[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-        f[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+    __device__ __forceinline__ void load(const void* base, size_t elem)
+    {
+        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(base) + elem * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); i++) {
+            const uint4 u = p[i];
+            w[4 * i] = u.x;
+            w[4 * i + 1] = u.y;
+            w[4 * i + 2] = u.z;
+            w[4 * i + 3] = u.w;
+        }
     }
+    __device__ __forceinline__ void store(void* base, size_t elem) const
+    {
+        uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(base) + elem * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); i++) p[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 4 : 8); i++) w[i] = 0;
+    }
+    __device__ __forceinline__ float at(int j) const
+    {
+        if (!BF16) return __uint_as_float(w[j]);
+        return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+    }
+    // this + a, rounded to the type
+    __device__ __forceinline__ void add(const Piece& a)
+    {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float lo = at(j) + a.at(j), hi = at(j + 1) + a.at(j + 1);
+            if (BF16) w[j / 2] = bf16x2_bits(lo, hi);
+            else {
+                w[j] = __float_as_uint(lo);
+                w[j + 1] = __float_as_uint(hi);
+            }
+        }
+    }
+};
+
+// v * g * r rounded once, r = rh + rl: the product as a sum of two floats each (FMA gives the
+// products' remainders), which is off by less than 2^-44 before the rounding; where something
+// could underflow or is not finite, in double.
+__device__ __forceinline__ float scaled(float v, float g, double r, float rh, float rl)
+{
+    const float p = v * g, e = fmaf(v, g, -p);
+    const float hi = p * rh;
+    const float lo = fmaf(e, rh, fmaf(p, rl, fmaf(p, rh, -hi)));
+    const float n = hi + lo;
+    if (fabsf(p) > 0x1p-90f && fabsf(hi) > 0x1p-90f && fabsf(hi) < 0x1p90f && rh < 0x1p90f && rh > 0x1p-60f) return n;
+    return (float)((double)v * (double)g * r);
 }
 
 // One CTA per row, blockDim.x a multiple of 32, STEPS * blockDim.x * 8 >= H.  x may alias
 // sum, and so may the residual: each element is read and written by the same thread.
-template <bool BF16, int STEPS>
-__global__ void __launch_bounds__(STEPS == 4 ? 1024 : 768) fp8_norm_kernel(Fp8NormParams p)
+template <bool BF16, int STEPS, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) fp8_norm_kernel(Fp8NormParams p)
 {
     __shared__ double part[32];
     const int nthr = blockDim.x, tid = threadIdx.x;
     const size_t row = (size_t)blockIdx.x * p.H;
-    Row8 r[STEPS];
+    Piece<BF16> x[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; i++) {
+        const int c = (i * nthr + tid) * 8;
+        x[i].clear();
+        if (c < p.H) x[i].load(p.x, row + c);
+    }
+    if (p.residual) {
+        Piece<BF16> a[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; i++) {
+            const int c = (i * nthr + tid) * 8;
+            a[i].clear();
+            if (c < p.H) a[i].load(p.residual, row + c);
+        }
+#pragma unroll
+        for (int i = 0; i < STEPS; i++) x[i].add(a[i]);
+    }
     double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < STEPS; i++) {
         const int c = (i * nthr + tid) * 8;
-        if (c < p.H) {
-            r[i] = load8<BF16>(p.x, row + c);
-            if (p.residual) {
-                const Row8 a = load8<BF16>(p.residual, row + c);
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float s = r[i].v[j] + a.v[j];
-                    r[i].v[j] = BF16 ? __bfloat162float(__float2bfloat16_rn(s)) : s;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; j++) r[i].v[j] = 0.0f;
-        }
+        if (p.sum && c < p.H) x[i].store(p.sum, row + c);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const double d = r[i].v[j];
+            const double d = x[i].at(j);
             ss = fma(d, d, ss);
-        }
-    }
-    if (p.sum) {
-#pragma unroll
-        for (int i = 0; i < STEPS; i++) {
-            const int c = (i * nthr + tid) * 8;
-            if (c < p.H) store8<BF16>(p.sum, row + c, r[i]);
         }
     }
 #pragma unroll
@@ -109,39 +130,34 @@ __global__ void __launch_bounds__(STEPS == 4 ? 1024 : 768) fp8_norm_kernel(Fp8No
     __syncthreads();
     double tot = 0.0;
     for (int w = 0; w < nthr / 32; w++) tot += part[w];
-    const double rinv = 1.0 / sqrt(tot / (double)p.H + p.eps);
+    const double r = 1.0 / sqrt(tot / (double)p.H + p.eps);
+    const float rh = (float)r, rl = (float)(r - (double)rh);
     const int nb = fp8_blocks(p.H);
 #pragma unroll
     for (int i = 0; i < STEPS; i++) {
         const int c = (i * nthr + tid) * 8;
         const bool in = c < p.H;
-        float g[8];
-        if (p.gamma && in) {
-            const Row8 gr = load8<false>(p.gamma, c);
-#pragma unroll
-            for (int j = 0; j < 8; j++) g[j] = gr.v[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; j++) g[j] = 1.0f;
-        }
+        Piece<false> g;
+        if (p.gamma && in) g.load(p.gamma, c);
+        Row8 n;
         uint32_t top = 0;      // bits of the largest |n|; a NaN's bits are above every number's
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            r[i].v[j] = in ? (float)((double)r[i].v[j] * rinv * (double)g[j]) : 0.0f;
-            top = max(top, __float_as_uint(r[i].v[j]) & 0x7FFFFFFFu);
+            n.v[j] = in ? scaled(x[i].at(j), p.gamma ? g.at(j) : 1.0f, r, rh, rl) : 0.0f;
+            top = max(top, __float_as_uint(n.v[j]) & 0x7FFFFFFFu);
         }
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (!in) continue;
-        if (p.out) store8<false>(p.out, row + c, r[i]);
-        const Quantizer qz(top);
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const float* f = r[i].v + 4 * h;
-            w[h] = qz.codes(f[0], f[1]) | qz.codes(f[2], f[3]) << 16;
+        if (p.out) {
+            float4* f = reinterpret_cast<float4*>(p.out + row + c);
+            f[0] = make_float4(n.v[0], n.v[1], n.v[2], n.v[3]);
+            f[1] = make_float4(n.v[4], n.v[5], n.v[6], n.v[7]);
         }
-        *reinterpret_cast<uint2*>(p.q + row + c) = make_uint2(w[0], w[1]);
+        const Quantizer qz(top);
+        const uint32_t lo = qz.codes(n.v[0], n.v[1]) | qz.codes(n.v[2], n.v[3]) << 16;
+        const uint32_t hi = qz.codes(n.v[4], n.v[5]) | qz.codes(n.v[6], n.v[7]) << 16;
+        *reinterpret_cast<uint2*>(p.q + row + c) = make_uint2(lo, hi);
         if ((tid & 15) == 0) p.scales[(size_t)blockIdx.x * nb + c / kFp8Block] = qz.scale;
     }
 }
@@ -150,13 +166,18 @@ template <bool BF16>
 cudaError_t launch(const Fp8NormParams& p, int num_sms, cudaStream_t s)
 {
     const int chunks = (p.H + 7) / 8;                 // 8-column pieces of a row
-    // With few rows a piece a thread, for the shortest way through a row; with many, four, so
-    // that more rows are on an SM and one's loads run beside another's reduction.
+    // With few rows a piece a thread, for the shortest way through a row.  With many, up to
+    // four pieces a thread and about 256 threads, so that five rows are on an SM and one's loads
+    // run beside another's reduction (8192 x 6144 bf16: 3 pieces 106 us, 2 pieces 110, 4 pieces
+    // 130, 1 piece 128; six rows an SM spill, 118).
     auto threads = [&](int steps) { return ((chunks + steps - 1) / steps + 31) / 32 * 32; };
-    if (p.T > 2 * num_sms && chunks >= 128) fp8_norm_kernel<BF16, 4><<<p.T, threads(4), 0, s>>>(p);
-    else if (chunks <= 768) fp8_norm_kernel<BF16, 1><<<p.T, threads(1), 0, s>>>(p);
-    else if (chunks <= 1536) fp8_norm_kernel<BF16, 2><<<p.T, threads(2), 0, s>>>(p);
-    else fp8_norm_kernel<BF16, 4><<<p.T, threads(4), 0, s>>>(p);
+    const int many = p.T > 2 * num_sms ? (chunks + 255) / 256 : 0;
+    if (many == 2) fp8_norm_kernel<BF16, 2, 256, 5><<<p.T, threads(2), 0, s>>>(p);
+    else if (many == 3) fp8_norm_kernel<BF16, 3, 256, 5><<<p.T, threads(3), 0, s>>>(p);
+    else if (many == 4) fp8_norm_kernel<BF16, 4, 256, 4><<<p.T, threads(4), 0, s>>>(p);
+    else if (chunks <= 768) fp8_norm_kernel<BF16, 1, 768, 1><<<p.T, threads(1), 0, s>>>(p);
+    else if (chunks <= 1536) fp8_norm_kernel<BF16, 2, 768, 1><<<p.T, threads(2), 0, s>>>(p);
+    else fp8_norm_kernel<BF16, 4, 1024, 1><<<p.T, threads(4), 0, s>>>(p);
     return cudaGetLastError();
 }
 
