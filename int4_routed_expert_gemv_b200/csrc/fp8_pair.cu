@@ -149,7 +149,7 @@ __device__ __forceinline__ void scaled_add(float* acc, const uint32_t (&v)[16], 
 // memory, 128 bytes each at a time, so that 8 neighbouring lanes write 128 (64 for bf16 with
 // a residual) consecutive bytes.  The residual was brought into L2 when the tile began; the 8
 // loads of a piece are under way together.
-template <class Y>
+template <class Y, bool RES>
 __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, const float (&acc)[C],
                                            uint8_t* stage, int lane)
 {
@@ -174,14 +174,14 @@ __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, in
                 for (int r = 0; r < 8; r++) {
                     const int to = __shfl_sync(0xffffffffu, orow, r0 + r);
                     at[r] = to >= 0 && in ? (size_t)to * rows + col : ~(size_t)0;
-                    v[r] = f[(r0 + r) * P + lane] + (residual && at[r] != ~(size_t)0 ? (float)residual[at[r]] : 0.0f);
+                    v[r] = f[(r0 + r) * P + lane] + (RES && at[r] != ~(size_t)0 ? (float)residual[at[r]] : 0.0f);
                 }
 #pragma unroll
                 for (int r = 0; r < 8; r++)
                     if (at[r] != ~(size_t)0) y[at[r]] = (Y)v[r];
             }
         }
-    } else if (ES == 2 && !residual) {
+    } else if (ES == 2 && !RES) {
 #pragma unroll
         for (int j0 = 0; j0 < C; j0 += 64) {
             const int col = c0 + (j0 >> 6) * kM + piece * 8;
@@ -203,24 +203,27 @@ __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, in
     } else {
         using R = typename std::conditional<ES == 4, float4, uint2>::type;    // 4 columns of the residual
         auto col_of = [&](int j0) { return c0 + (j0 >> 6) * kM + (j0 & 63) + piece * 4; };
+        R res[2][8];
+        auto fetch = [&](int j0, R (&to)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int r = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
+                to[i] = R{};
+                if (r >= 0 && col_of(j0) < rows) to[i] = *reinterpret_cast<const R*>(residual + (size_t)r * rows + col_of(j0));
+            }
+        };
+        if (RES) fetch(0, res[0]);
 #pragma unroll
         for (int j0 = 0; j0 < C; j0 += 32) {
-            R res[8];
-            if (residual) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int r = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
-                    res[i] = R{};
-                    if (r >= 0 && col_of(j0) < rows)
-                        res[i] = *reinterpret_cast<const R*>(residual + (size_t)r * rows + col_of(j0));
-                }
-            }
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < 8; c++)
                 *reinterpret_cast<float4*>(stage + lane * kPitch + c * 16) =
                     make_float4(acc[j0 + 4 * c], acc[j0 + 4 * c + 1], acc[j0 + 4 * c + 2], acc[j0 + 4 * c + 3]);
             __syncwarp();
+            // the next run's loads, ahead of this one's stores, take the registers of the sums just
+            // staged
+            if (RES && j0 + 32 < C) fetch(j0 + 32, res[(j0 / 32 + 1) & 1]);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
@@ -228,13 +231,13 @@ __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, in
                 if (to < 0 || col_of(j0) >= rows) continue;
                 Y* at = y + (size_t)to * rows + col_of(j0);
                 if constexpr (ES == 4) {
-                    if (residual) {
-                        const float4 a = res[i];
+                    if (RES) {
+                        const float4 a = res[j0 / 32 & 1][i];
                         v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
                     }
                     *reinterpret_cast<float4*>(at) = v;
                 } else {
-                    const uint2 a = res[i];
+                    const uint2 a = res[j0 / 32 & 1][i];
                     *reinterpret_cast<uint2*>(at) =
                         make_uint2(bf16x2_bits(v.x + __uint_as_float(a.x << 16), v.y + __uint_as_float(a.x & 0xFFFF0000u)),
                                    bf16x2_bits(v.z + __uint_as_float(a.y << 16), v.w + __uint_as_float(a.y & 0xFFFF0000u)));
@@ -552,17 +555,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (left <= 0) continue;
                 // output columns of the thread's two runs of 64
                 const int c0 = 2 * w.rb * kM + wg * 64;
-                if (MODE == FP8_DOWN) store_rows<float>(p.z, nullptr, p.rows, c0, w.orow, acc, stage, lane);
-                else if (p.slices > 1)
-                    store_rows<float>(p.partial + (size_t)it.slice * p.T * p.pitch, nullptr, p.pitch, c0, w.orow, acc, stage,
-                                      lane);
-                else if (p.y_bf16)
-                    store_rows<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.y),
-                                              reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.orow, acc,
-                                              stage, lane);
-                else
-                    store_rows<float>(reinterpret_cast<float*>(p.y), reinterpret_cast<const float*>(p.residual), p.rows, c0,
-                                      w.orow, acc, stage, lane);
+                const auto store = [&](auto* y, auto res) {
+                    using Y = std::remove_pointer_t<decltype(y)>;
+                    const Y* r = reinterpret_cast<const Y*>(p.residual);
+                    store_rows<Y, decltype(res)::value>(y, r, MODE == FP8_DENSE && p.slices > 1 ? p.pitch : p.rows, c0, w.orow,
+                                                        acc, stage, lane);
+                };
+                constexpr std::false_type none{};
+                constexpr std::true_type with{};
+                if (MODE == FP8_DOWN) store(p.z, none);
+                else if (p.slices > 1) store(p.partial + (size_t)it.slice * p.T * p.pitch, none);
+                else if (p.y_bf16 && p.residual) store(reinterpret_cast<__nv_bfloat16*>(p.y), with);
+                else if (p.y_bf16) store(reinterpret_cast<__nv_bfloat16*>(p.y), none);
+                else if (p.residual) store(reinterpret_cast<float*>(p.y), with);
+                else store(reinterpret_cast<float*>(p.y), none);
             } else {
                 // SwiGLU of 64 columns; the scale block is this and the other warpgroup's
                 uint32_t top = 0;
