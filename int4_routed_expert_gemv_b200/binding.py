@@ -60,6 +60,8 @@ _lib = None
 def lib():
     """Load libcolimoe.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -277,9 +279,13 @@ def coli_rmsnorm(hidden, T, x, gamma, eps, out, stream=None) -> int:
 
 # 8-bit floating point path: codes are torch.float8_e4m3fn (or uint8) tensors, scales fp32.
 
+# The norm runs in few microseconds, so its marshalling is written out.
+
 def coli_rmsnorm_fp8(hidden, T, x, residual, gamma, eps, sum, out, q, scales, stream=None) -> int:
-    return lib().coli_rmsnorm_fp8(hidden, T, _p(x), _p(residual), _dt(x), _p(gamma), float(eps), _p(sum), _p(out),
-                                  _p(q), _p(scales), _s(stream))
+    return lib().coli_rmsnorm_fp8(hidden, T, x.data_ptr(), None if residual is None else residual.data_ptr(), _dt(x),
+                                  None if gamma is None else gamma.data_ptr(), eps,
+                                  None if sum is None else sum.data_ptr(), None if out is None else out.data_ptr(),
+                                  q.data_ptr(), scales.data_ptr(), _s(stream))
 
 
 def coli_fp8_workspace_bytes(T: int, N: int, K: int) -> int:

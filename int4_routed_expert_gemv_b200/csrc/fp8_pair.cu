@@ -46,7 +46,7 @@ constexpr uint32_t kStage = 2 * kTile;
 constexpr int kStages = 5;
 constexpr int kBufs = 2;
 constexpr uint32_t kTmem = kBufs * 256;
-constexpr int kBox = 64;                          // rows of a token box
+constexpr int kBox = 128;                         // rows of a token box
 constexpr int kLeast = 6;                         // K steps of a run at least
 constexpr int kJoin = 12;                         // what joining the parts of a tile costs, in K steps
 constexpr int kPitch = 144;                       // bytes of a staged row: 128 and a gap

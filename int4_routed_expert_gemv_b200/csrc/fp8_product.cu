@@ -160,7 +160,7 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     memset(&p, 0, sizeof(p));
     const bool decode = a.T <= kDecodeTokens;
     // rows of a token box (1: rows gathered one by one)
-    const int box = !decode ? 64 : a.mode == FP8_DOWN ? 1 : 16;
+    const int box = !decode ? 128 : a.mode == FP8_DOWN ? 1 : 16;
     uint8_t* gathered = a.scratch + partial_bytes(a.T);
     bool ok = true;
     if (a.mode == FP8_DENSE) {
