@@ -235,9 +235,17 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// silu(g) * u: expf and the quotient are within 2 ulp each; the quotient's 0 for 1 + exp(-g)
-// above 2^126 is off by less than the smallest normal number.
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
+// silu(g) * u.  The quotient g / (1 + exp(-g)) is an approximate reciprocal's with one correction
+// by its remainder (as Quantizer's), so it is off by little more than its rounding; where the
+// denominator is so large that the reciprocal could underflow, the quotient is 0 to within the
+// smallest normal number (and NaN for g = -inf, like -inf / inf).
+__device__ __forceinline__ float swiglu(float g, float u)
+{
+    const float d = 1.0f + expf(-g);
+    const float r = __fdividef(1.0f, d), q = g * r;
+    const float s = d >= 0x1p120f ? g * 0.0f : fmaf(fmaf(-q, d, g), r, q);
+    return s * u;
+}
 
 // One thread, after its CTA's barrier: counts a part of a tile whose sums the CTA has stored.
 // True for the last of `parts`, which then sees the others' sums; the counter is 0 again.

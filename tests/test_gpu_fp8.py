@@ -79,6 +79,21 @@ def test_matmul_repeats_bitwise(colimoe):
         assert all(torch.equal(ys[0], y) for y in ys[1:])
 
 
+def test_matmul_more_than_32_bits_of_outputs(colimoe):
+    # T * N passes 2^31: the last rows, and rows on both sides of the border
+    T, N, K = 66000, 33000, 16
+    g = torch.Generator().manual_seed(11)
+    xq, xs = R.activations(T, K, g)
+    wq, s = R.weights(N, K, g)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    B.check(B.coli_fp8_matmul(T, N, K, xq.cuda(), xs.cuda(), wq.cuda(), s.cuda(), None, y, dense_ws(T, N, K)))
+    rows = torch.tensor([0, 65074, 65075, 65076, T - 1])
+    x, w = R.dequant(xq[rows], xs[rows]), R.dequant_w(wq, s)
+    ref, mag = x @ w.T, x.abs() @ w.abs().T
+    bound = mag * R.product_bound(1) + (ref.abs() + mag * R.product_bound(1)) * 2.0 ** -8
+    assert ((y[rows.cuda()].cpu().double() - ref).abs() <= bound).all()
+
+
 def test_matmul_in_place_residual(colimoe):
     g = torch.Generator().manual_seed(4)
     T, N, K = 33, 257, 512
@@ -157,6 +172,18 @@ def test_norm(colimoe, dtype, T, H, residual, router):
         assert torch.equal(sm[:T].cpu(), x)      # the sum of x alone is x
     check_norm(x, r, gamma, 1e-5, sm[:T].cpu() if residual else None, out[:T].cpu() if router else None,
                q[:T].cpu().view(R.E4M3), s[:T].cpu())
+
+
+def test_norm_more_than_32_bits_of_elements(colimoe):
+    T, H = 140000, 16384
+    x = torch.randn(1000, H, device="cuda", dtype=torch.bfloat16, generator=torch.Generator("cuda").manual_seed(2))
+    x = x.repeat(140, 1)
+    x[T - 1] *= 3
+    q = torch.empty(T, H, dtype=R.E4M3, device="cuda")
+    s = torch.empty(T, H // 128, device="cuda")
+    B.check(B.coli_rmsnorm_fp8(H, T, x, None, None, 1e-5, None, None, q, s))
+    rows = torch.tensor([0, 131071, 131072, T - 1])
+    check_norm(x[rows.cuda()].cpu(), None, None, 1e-5, None, None, q[rows.cuda()].cpu(), s[rows.cuda()].cpu())
 
 
 @pytest.mark.parametrize("which", ["x", "residual"])
@@ -405,6 +432,42 @@ def test_norm_route_experts_together(colimoe, T):
         got = y.clone()
         step()
         assert torch.equal(got, y)
+
+
+def test_quantised_layer_is_near_the_layer(colimoe):
+    """fp32 expert weights through the host quantiser, and the experts on the quantised rows of a norm: within the
+    codes' precision of the fp32 layer (each product's terms are off by 2^-4 at most on either side, and h's codes
+    by 2^-4 again; independent errors of a sum of many terms come out far below their sum)."""
+    import numpy as np
+    from int4_routed_expert_gemv_b200 import quantize as Q
+    H, I, E, k, T = 256, 192, 6, 2, 20
+    rng = np.random.default_rng(5)
+    mats = [[rng.standard_normal(s).astype(np.float32) / s[1] ** 0.5 for s in ((I, H), (I, H), (H, I))] for _ in range(E)]
+    stride = (B.coli_moe_blob_bytes_fp8(H, I) + 255) // 256 * 256
+    blobs = torch.zeros(E, stride, dtype=torch.uint8)
+    for e in range(E):
+        b, _ = Q.expert_blob_fp8(*mats[e])
+        blobs[e, :b.size] = torch.from_numpy(b)
+    idx = torch.from_numpy(rng.permuted(np.tile(np.arange(E), (T, 1)), axis=1)[:, :k].astype(np.int32))
+    w = torch.softmax(torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)), 1)
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).cuda()
+    dims = B.make_dims(H, I, E, k, 0)
+    dev = blobs.cuda()
+    weights = B.make_weights(None, None, dev, None, stride)
+    ws = torch.zeros(B.coli_moe_workspace_bytes_fp8(dims, T), dtype=torch.uint8, device="cuda")
+    B.check(B.coli_moe_workspace_init(ws))
+    n, q, s = torch.empty_like(x), torch.empty(T, H, dtype=R.E4M3, device="cuda"), torch.empty(T, 2, device="cuda")
+    y = torch.empty_like(x)
+    B.check(B.coli_rmsnorm_fp8(H, T, x, None, None, 1e-6, None, n, q, s))
+    B.check(B.coli_moe_forward_fp8(dims, weights, q, s, T, w.cuda(), *[t.cuda() for t in R.lists(idx, E)], None, y, ws))
+    nn = n.cpu().double().numpy()
+    ref = np.zeros((T, H))
+    for t in range(T):
+        for j in range(k):
+            G, U, D = (m.astype(np.float64) for m in mats[int(idx[t, j])])
+            g = G @ nn[t]
+            ref[t] += float(w[t, j]) * (D @ (g / (1 + np.exp(-g)) * (U @ nn[t])))
+    assert np.linalg.norm(y.cpu().double().numpy() - ref) < 2.0 ** -3 * np.linalg.norm(ref)
 
 
 def test_other_streams(colimoe):
