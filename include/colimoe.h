@@ -317,7 +317,9 @@ COLI_API coli_status coli_rmsnorm(int32_t hidden, int32_t T, const float* x, con
  * (every code of a block with a NaN).
  * Products accumulate in fp32: the 128 terms of a scale block on the tensor cores, then
  * times both scales, block after block in a fixed order (split over several blocks of the
- * grid where there are few tiles; still one fixed order for given sizes and device).
+ * grid where there are few tiles; still one fixed order for given sizes and device).  The
+ * format is that of the fp8 checkpoints which the int4 containers are converted from
+ * (colibri README.zh-CN "开始使用 / 2. 获取模型").
  * The fp8 calls share one kind of workspace among themselves; init it with
  * coli_moe_workspace_init, read errors with coli_moe_read_status (COLI_DEV_BAD_INDEX: lists
  * outside the batch; what they name is then neither read nor written), and keep calls
@@ -325,7 +327,8 @@ COLI_API coli_status coli_rmsnorm(int32_t hidden, int32_t T, const float* x, con
 
 /* Residual addition, RMSNorm and quantisation in one pass:
  *   s = x + residual, rounded once to dtype (x itself without a residual);  sum = s;
- *   n = s * gamma / sqrt(mean(s^2) + eps), computed in double and rounded once to fp32;
+ *   n = s * gamma / sqrt(mean(s^2) + eps), rounded to fp32 (sum and root in double; the result
+ *   within half a step and 2^-40 of the exact value);
  *   out = n;  q, scales = the quantised rows of n.
  * x, residual, sum [T][hidden] in dtype (residual and sum may be NULL; sum may be x or
  * residual), gamma [hidden] fp32 or NULL (all ones), out [T][hidden] fp32 or NULL, q
@@ -367,7 +370,8 @@ COLI_API coli_status coli_moe_gate_up_fp8(const coli_moe_dims* dims, const coli_
 
 /* The experts' second product and the combine: y [T][H] fp32 = residual + D_shared h + sum
  * over slots of w[t][slot] * D_e h, h = (hq, hs) as coli_moe_gate_up_fp8 leaves them.  The
- * terms of a token are added in slot order; a slot that the lists leave out adds nothing.
+ * terms of a token are added in one fixed order (T <= 16: shared, then by expert; above: by
+ * slot); a slot that the lists leave out adds nothing.
  * residual [T][H] fp32 or NULL, may be y. */
 COLI_API coli_status coli_moe_down_fp8(const coli_moe_dims* dims, const coli_moe_weights* weights,
                                        const uint8_t* hq, const float* hs, int32_t T, const float* w,
