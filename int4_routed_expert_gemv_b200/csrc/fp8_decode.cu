@@ -46,7 +46,7 @@ constexpr int kMaxPos = NT * 32;        // positions of the union lists: 16 toke
 constexpr uint32_t kSite = 60;
 
 struct Tables {
-    Groups g;
+    Groups<kMaxGroups> g;
     int pos[kMaxPos];                   // t * k + slot of each list position (-1: not of this batch)
     float wt[kMaxPos];                  // routing weights [t * k + slot]
 };

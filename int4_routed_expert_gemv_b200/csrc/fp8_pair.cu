@@ -43,16 +43,41 @@ constexpr int NT = 256;                           // tokens of a tile
 constexpr int C = 128;                            // columns of a thread
 constexpr uint32_t kTile = kM * 128;              // bytes of a CTA's tokens or weights per K step
 constexpr uint32_t kStage = 2 * kTile;
-constexpr int kStages = 5;
 constexpr int kBufs = 2;
 constexpr uint32_t kTmem = kBufs * 256;
 constexpr int kBox = 128;                         // rows of a token box
 constexpr int kLeast = 6;                         // K steps of a run at least
 constexpr int kJoin = 12;                         // what joining the parts of a tile costs, in K steps
-constexpr int kPitch = 144;                       // bytes of a staged row: 128 and a gap
-constexpr size_t kOut = (size_t)kEpi * kPitch;
-constexpr size_t kSmem = 1024 + kStages * (size_t)kStage + kOut + 2 * kM * 4 +
-                         (kMaxGroups + 3) / 4 * 4 * 4 + sizeof(Groups) + 16 + 16 + 256;
+constexpr uint32_t kOutBox = 32 * 128;            // a warp's 32 rows of 128 bytes of output
+
+// Three stages are enough (two, three and four more gain nothing: what bounds the copies is the
+// shared memory they share with the MMA's reads), which leaves room for a tile's outputs.
+template <int MODE>
+struct Shape {
+    static constexpr int kStages = MODE == FP8_GATE_UP ? 4 : 3;
+    static constexpr int kBoxes = MODE == FP8_DENSE ? 4 : MODE == FP8_DOWN ? 3 : 0;      // output boxes of a warp
+    static constexpr int kGroups = MODE == FP8_DENSE ? 1 : kMaxGroups;
+};
+
+template <int MODE>
+struct Smem {
+    using S = Shape<MODE>;
+    uint8_t stage[S::kStages][kStage];
+    uint8_t box[kEpi / 32][S::kBoxes > 0 ? S::kBoxes : 1][S::kBoxes > 0 ? kOutBox : 16];
+    uint32_t top[2][kM];                 // maxima of the SwiGLU rows, by warpgroup
+    Groups<S::kGroups> groups;
+    int first[S::kGroups];
+    int n_groups, tiles, last;
+    uint32_t tmem;
+    uint64_t full[S::kStages];           // rank 0: both CTAs' tiles landed
+    uint64_t empty[S::kStages];          // MMAs done with the stage
+    uint64_t acc_full[kBufs];            // MMA commit
+    uint64_t acc_empty[kBufs];           // rank 0: read by every accumulating warp of the pair
+    uint64_t mma_done[2];
+    uint64_t res[kEpi / 32];             // a warp's part of the residual landed
+};
+template <int MODE>
+constexpr size_t kSmem = sizeof(Smem<MODE>) + 1024;
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -144,147 +169,174 @@ __device__ __forceinline__ void scaled_add(float* acc, const uint32_t (&v)[16], 
     for (int j = 0; j < 16; j++) acc[j] = fmaf(__uint_as_float(v[j]), s, acc[j]);
 }
 
-// A warp's 32 rows of outputs, one per thread (orow: its row of y, -1 for none): two runs of 64
-// columns, at c0 and c0 + 128, plus the residual, rounded once.  Rows go through shared
-// memory, 128 bytes each at a time, so that 8 neighbouring lanes write 128 (64 for bf16 with
-// a residual) consecutive bytes.  The residual was brought into L2 when the tile began; the 8
-// loads of a piece are under way together.
-template <class Y, bool RES>
-__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, const float (&acc)[C],
-                                           uint8_t* stage, int lane)
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
 {
-    constexpr int ES = (int)sizeof(Y);
-    const int r4 = lane >> 3, piece = lane & 7;
-    if (rows % (16 / ES) != 0) {
-        // rows that do not begin on 16 bytes: 32 columns at a time, one lane a column
-        float* f = reinterpret_cast<float*>(stage);
-        constexpr int P = kPitch / 4;
+    tma_load_3d(dst, map, x, y, z, bar);
+}
+
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, int z, const void* src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(z), "r"(smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Until at most N of this thread's stores have still to read their boxes.
+template <int N>
+__device__ __forceinline__ void boxes_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// The columns of a warp's output: two runs of 64, at c0 and c0 + 128, in boxes of 128 bytes a row.
+template <class Y>
+struct Boxes {
+    static constexpr int W = 128 / (int)sizeof(Y), N = C / W;
+    __device__ static __forceinline__ int column(int c0, int j) { return c0 + j / (N / 2) * kM + j % (N / 2) * W; }
+};
+
+// One lane: the warp's part of the residual (rows from y0) into its boxes, once the stores before
+// have read them.
+template <class Y>
+__device__ __forceinline__ void ask_residual(const Params& p, int c0, int y0, uint8_t* box, uint64_t* bar)
+{
+    boxes_read<0>();
+    uint32_t bytes = 0;
 #pragma unroll
-        for (int j0 = 0; j0 < C; j0 += 32) {
-            const int col = c0 + (j0 >> 6) * kM + (j0 & 63) + lane;
-            const bool in = col < rows;
+    for (int j = 0; j < Boxes<Y>::N; j++) bytes += Boxes<Y>::column(c0, j) < p.rows ? kOutBox : 0;
+    mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+    for (int j = 0; j < Boxes<Y>::N; j++)
+        if (Boxes<Y>::column(c0, j) < p.rows) load_box(box + j * kOutBox, &p.res, Boxes<Y>::column(c0, j), y0, 0, bar);
+}
+
+// A warp's 32 rows of outputs, one per thread, to rows from y0 of the map (rows and columns
+// beyond its end are left out), plus the residual that its boxes hold, rounded once.  The copies
+// out run while the next tile's sums are formed.  With `ragged`, the first `left` rows only, by
+// the warp itself: the rows behind them are another tile's.
+template <class Y, bool RES, int NB>
+__device__ __forceinline__ void store_boxes(const CUtensorMap* map, int c0, int y0, int z, int rows, const float (&acc)[C],
+                                            uint8_t* box, int lane, Y* ragged = nullptr, int left = 32)
+{
+    constexpr int ES = (int)sizeof(Y), W = Boxes<Y>::W, N = Boxes<Y>::N;
+    if (!RES) {
+        if (lane == 0) boxes_read<0>();
+        __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+        if (Boxes<Y>::column(c0, j) >= rows) break;       // and all later ones
+        if (j >= NB) {
+            if (lane == 0) boxes_read<NB - 1>();
             __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 32; j++) f[lane * P + j] = acc[j0 + j];
-            __syncwarp();
-            for (int r0 = 0; r0 < 32; r0 += 8) {
-                float v[8];
-                size_t at[8];
-#pragma unroll
-                for (int r = 0; r < 8; r++) {
-                    const int to = __shfl_sync(0xffffffffu, orow, r0 + r);
-                    at[r] = to >= 0 && in ? (size_t)to * rows + col : ~(size_t)0;
-                    v[r] = f[(r0 + r) * P + lane] + (RES && at[r] != ~(size_t)0 ? (float)residual[at[r]] : 0.0f);
-                }
-#pragma unroll
-                for (int r = 0; r < 8; r++)
-                    if (at[r] != ~(size_t)0) y[at[r]] = (Y)v[r];
-            }
         }
-    } else if (ES == 2 && !RES) {
+        uint8_t* mine = box + (j % NB) * kOutBox + lane * 128;
 #pragma unroll
-        for (int j0 = 0; j0 < C; j0 += 64) {
-            const int col = c0 + (j0 >> 6) * kM + piece * 8;
-            __syncwarp();
+        for (int c = 0; c < 8; c++) {
+            uint4* at = reinterpret_cast<uint4*>(mine + ((c ^ (lane & 7)) << 4));      // 128-byte swizzle
+            const uint4 u = RES ? *at : make_uint4(0, 0, 0, 0);
+            const uint32_t r[4] = {u.x, u.y, u.z, u.w};
+            uint32_t w[4];
 #pragma unroll
-            for (int c = 0; c < 8; c++) {
-                const float* f = acc + j0 + 8 * c;
-                *reinterpret_cast<uint4*>(stage + lane * kPitch + c * 16) = make_uint4(
-                    bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]), bf16x2_bits(f[6], f[7]));
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + (i * 4 + r4) * kPitch + piece * 16);
-                if (to >= 0 && col < rows) *reinterpret_cast<uint4*>(y + (size_t)to * rows + col) = v;
-            }
-        }
-    } else {
-        using R = typename std::conditional<ES == 4, float4, uint2>::type;    // 4 columns of the residual
-        auto col_of = [&](int j0) { return c0 + (j0 >> 6) * kM + (j0 & 63) + piece * 4; };
-        R res[2][8];
-        auto fetch = [&](int j0, R (&to)[8]) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int r = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
-                to[i] = R{};
-                if (r >= 0 && col_of(j0) < rows) to[i] = *reinterpret_cast<const R*>(residual + (size_t)r * rows + col_of(j0));
-            }
-        };
-        if (RES) fetch(0, res[0]);
-#pragma unroll
-        for (int j0 = 0; j0 < C; j0 += 32) {
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 8; c++)
-                *reinterpret_cast<float4*>(stage + lane * kPitch + c * 16) =
-                    make_float4(acc[j0 + 4 * c], acc[j0 + 4 * c + 1], acc[j0 + 4 * c + 2], acc[j0 + 4 * c + 3]);
-            __syncwarp();
-            // the next run's loads, ahead of this one's stores, take the registers of the sums just
-            // staged
-            if (RES && j0 + 32 < C) fetch(j0 + 32, res[(j0 / 32 + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int to = __shfl_sync(0xffffffffu, orow, i * 4 + r4);
-                float4 v = *reinterpret_cast<const float4*>(stage + (i * 4 + r4) * kPitch + piece * 16);
-                if (to < 0 || col_of(j0) >= rows) continue;
-                Y* at = y + (size_t)to * rows + col_of(j0);
-                if constexpr (ES == 4) {
-                    if (RES) {
-                        const float4 a = res[j0 / 32 & 1][i];
-                        v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
-                    }
-                    *reinterpret_cast<float4*>(at) = v;
+            for (int e = 0; e < 4; e++) {
+                if (ES == 4) {
+                    const float f = acc[j * W + 4 * c + e];
+                    w[e] = __float_as_uint(RES ? f + __uint_as_float(r[e]) : f);
                 } else {
-                    const uint2 a = res[j0 / 32 & 1][i];
-                    *reinterpret_cast<uint2*>(at) =
-                        make_uint2(bf16x2_bits(v.x + __uint_as_float(a.x << 16), v.y + __uint_as_float(a.x & 0xFFFF0000u)),
-                                   bf16x2_bits(v.z + __uint_as_float(a.y << 16), v.w + __uint_as_float(a.y & 0xFFFF0000u)));
+                    float lo = acc[j * W + 8 * c + 2 * e], hi = acc[j * W + 8 * c + 2 * e + 1];
+                    if (RES) {
+                        lo += __uint_as_float(r[e] << 16);
+                        hi += __uint_as_float(r[e] & 0xFFFF0000u);
+                    }
+                    w[e] = bf16x2_bits(lo, hi);
                 }
             }
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (ragged) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int r = i * 4 + (lane >> 3), piece = lane & 7;
+                const uint4 v = *reinterpret_cast<const uint4*>(box + (j % NB) * kOutBox + r * 128 + ((piece ^ (r & 7)) << 4));
+                if (r < left)
+                    *reinterpret_cast<uint4*>(ragged + (size_t)(y0 + r) * rows + Boxes<Y>::column(c0, j) + piece * (16 / ES)) = v;
+            }
+            __syncwarp();
+            continue;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) store_box(map, Boxes<Y>::column(c0, j), y0, z, box + (j % NB) * kOutBox);
+    }
+}
+
+// The same without boxes, for rows that do not begin on 16 bytes and for a warp whose rows end
+// inside it (orow: a thread's row of y, -1 for none): 32 columns at a time go through shared
+// memory, so that a warp writes 32 consecutive values of a row.
+template <class Y>
+__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, const float (&acc)[C],
+                                           float* stage, int lane)
+{
+    constexpr int P = 33;
+    if (lane == 0) boxes_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int j0 = 0; j0 < C; j0 += 32) {
+        const int col = c0 + (j0 >> 6) * kM + (j0 & 63) + lane;
+        const bool in = col < rows;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; j++) stage[lane * P + j] = acc[j0 + j];
+        __syncwarp();
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+            float v[8];
+            size_t at[8];
+#pragma unroll
+            for (int r = 0; r < 8; r++) {
+                const int to = __shfl_sync(0xffffffffu, orow, r0 + r);
+                at[r] = to >= 0 && in ? (size_t)to * rows + col : ~(size_t)0;
+                v[r] = stage[(r0 + r) * P + lane] + (residual && at[r] != ~(size_t)0 ? (float)residual[at[r]] : 0.0f);
+            }
+#pragma unroll
+            for (int r = 0; r < 8; r++)
+                if (at[r] != ~(size_t)0) y[at[r]] = (Y)v[r];
         }
     }
+    __syncwarp();
+    fence_async_smem();      // later copies into the same memory
 }
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ Params p)
 {
+    using S = Shape<MODE>;
+    constexpr int kStages = S::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // the same offset in both CTAs of the pair: dynamic shared memory starts at one address in
     // every CTA of a launch
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* out_stage = smem + kStages * (size_t)kStage;
-    uint32_t* tops = reinterpret_cast<uint32_t*>(out_stage + kOut);          // [2][kM] maxima of the SwiGLU rows
-    int* first = reinterpret_cast<int*>(tops + 2 * kM);
-    Groups& groups = *reinterpret_cast<Groups*>(first + (kMaxGroups + 3) / 4 * 4);
-    // [0] groups [1] tiles [2] last part [3] tensor memory
-    int* flags = reinterpret_cast<int*>((reinterpret_cast<uintptr_t>(&groups + 1) + 15) & ~uintptr_t(15));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(flags + 4);
-    uint64_t* full = bars;                       // [kStages] rank 0: both CTAs' tiles landed
-    uint64_t* empty = full + kStages;            // [kStages] MMAs done with the stage
-    uint64_t* acc_full = empty + kStages;        // [kBufs] MMA commit
-    uint64_t* acc_empty = acc_full + kBufs;      // [kBufs] rank 0: read by every accumulating warp of the pair
-    uint64_t* mma_done = acc_empty + kBufs;      // [2]
-
+    Smem<MODE>& sm =
+        *reinterpret_cast<Smem<MODE>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank();
     if (tid == 0) {
         for (int s = 0; s < kStages; s++) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
         }
         for (int b = 0; b < kBufs; b++) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 2 * kEpi / 32);
+            mbar_init(&sm.acc_full[b], 1);
+            mbar_init(&sm.acc_empty[b], 2 * kEpi / 32);
         }
-        mbar_init(&mma_done[0], 1);
-        mbar_init(&mma_done[1], 1);
+        mbar_init(&sm.mma_done[0], 1);
+        mbar_init(&sm.mma_done[1], 1);
+        for (int w = 0; w < kEpi / 32; w++) mbar_init(&sm.res[w], 1);
         fence_barrier_init();
     }
     if (warp == 9) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&flags[3])),
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)),
                      "r"(kTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -292,21 +344,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     pdl_wait();
     if (warp == 8) {
-        const int ng = read_groups<MODE>(p, lane, groups);
-        const int tiles = plan_tiles(p, groups, ng, NT, lane, first);
+        const int ng = read_groups<MODE>(p, lane, sm.groups);
+        const int tiles = plan_tiles(p, sm.groups, ng, NT, lane, sm.first);
         if (lane == 0) {
-            flags[0] = ng;
-            flags[1] = tiles;
+            sm.n_groups = ng;
+            sm.tiles = tiles;
         }
     }
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = (uint32_t)flags[3];
-    const int n_groups = flags[0];
+    const uint32_t tmem = sm.tmem;
+    const int n_groups = sm.n_groups;
     Schedule sch;
-    sch.init(flags[1], p.kb, (int)n_clusters(), (int)cluster_id(), kLeast, kJoin, p.slices);
+    sch.init(sm.tiles, p.kb, (int)n_clusters(), (int)cluster_id(), kLeast, kJoin, p.slices);
     bool dead = false;
     Item it;
 
@@ -316,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // ----------------------------- TMA producer ---------------------------------
             uint32_t n = 0;
             while (sch.next(it)) {
-                const Tile tl = tile_of(p, groups, first, n_groups, NT, it.tile);
+                const Tile tl = tile_of(p, sm.groups, sm.first, n_groups, NT, it.tile);
                 const int shared = tl.g.expert < 0 ? 1 : 0;
                 const CUtensorMap* wm = &p.w[shared];
                 const CUtensorMap* xm = &p.x[MODE == FP8_GATE_UP ? shared : 0];
@@ -330,12 +382,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int row0 = base + tl.t0 + rank * kM;
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int s = n % kStages;
-                    if (!dead && !mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
+                    if (!dead && !mbar_wait(&sm.empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
                     if (dead) continue;
                     if (lane == 0) {
-                        uint8_t* st = smem + (size_t)s * kStage;
-                        const uint32_t bar = map_to(&full[s], 0);
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                        uint8_t* st = sm.stage[s];
+                        const uint32_t bar = map_to(&sm.full[s], 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], bytes);
                         pair_load_3d(st + kTile, wm, kb * 128, r0, z, bar);
                         for (int b = 0; b < boxes; b++)
                             pair_load_2d(st + b * kBox * 128, xm, kb * 128, row0 + b * kBox, bar);
@@ -348,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t last = n < (uint32_t)kStages ? n : (uint32_t)kStages;
                 for (uint32_t i = 0; i < last; i++) {
                     const uint32_t m = n - 1 - i;
-                    mbar_wait(&full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
+                    mbar_wait(&sm.full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
                 }
             }
         } else if (warp == 9 || warp == 11) {
@@ -363,22 +415,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                         if ((n & 1) != odd) continue;
                         const int s = n % kStages, b = n % kBufs;
-                        const uint8_t* st = smem + (size_t)s * kStage;
+                        const uint8_t* st = sm.stage[s];
                         const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + kTile);
-                        if (!dead && !mbar_wait(&full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
-                        if (!dead && !mbar_wait(&acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
+                        if (!dead && !mbar_wait(&sm.full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
+                        if (!dead && !mbar_wait(&sm.acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
                         tc_fence_after();
                         if (!dead) {
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)      // 32 e4m3 values = 32 bytes per MMA
                                 umma_pair(tmem + (uint32_t)(b * 256), ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
                         }
-                        commit_pair(&acc_full[b]);
-                        commit_pair(&empty[s]);
+                        commit_pair(&sm.acc_full[b]);
+                        commit_pair(&sm.empty[s]);
                     }
                 }
-                commit_pair(&mma_done[odd]);
-                mbar_wait(&mma_done[odd], 0, p.status, kSite + 5);
+                commit_pair(&sm.mma_done[odd]);
+                mbar_wait(&sm.mma_done[odd], 0, p.status, kSite + 5);
             }
         }
     } else {
@@ -388,9 +440,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int row = q * 32 + lane;              // token within the CTA's 128
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         float acc[C];
-        uint8_t* stage = out_stage + warp * 32 * kPitch;
+        uint32_t asked = 0;                         // residual parts asked for
         uint32_t n = 0;
-        const uint32_t ae = map_to(&acc_empty[0], 0);
+        const uint32_t ae = map_to(&sm.acc_empty[0], 0);
         const int nb = fp8_blocks(p.rows);
         // What a tile needs besides its sums.  The next tile's is looked up (list positions, then
         // scales: loads that wait for one another) before this one's outputs are written.
@@ -398,6 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Item it;
             int rb, expert, left;        // row block, expert, tokens of this warp
             int xrow, orow;              // row of the token's scales, row of y / h / z (-1: none)
+            int y0;                      // the warp's first row of y / z
         };
         float xn[4], an[4], bn[4];       // scales of four K steps: token, both row blocks
         auto fetch = [&](const Work& w, int kb) {      // kb: a multiple of 4
@@ -427,13 +480,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         auto look_up = [&](Work& w) {
             if (!sch.next(w.it)) return false;
-            const Tile tl = tile_of(p, groups, first, n_groups, NT, w.it.tile);
+            const Tile tl = tile_of(p, sm.groups, sm.first, n_groups, NT, w.it.tile);
             w.rb = tl.rb;
             w.expert = tl.g.expert;
             w.left = tl.n - rank * kM - q * 32;
             const int tok = tl.t0 + rank * kM + row;            // token of the group
             w.xrow = 0;
             w.orow = -1;
+            w.y0 = (MODE == FP8_DENSE ? 0 : tl.g.base) + tok - lane;
             if (lane < w.left) {
                 if (MODE == FP8_DENSE) {
                     w.xrow = w.orow = tok;
@@ -443,22 +497,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 } else {
                     const int a = position_of(p, tl.g.base + tok);
                     w.xrow = MODE == FP8_DOWN ? tl.g.base + tok : max(a, 0) / p.k;
-                    if (a >= 0) w.orow = MODE == FP8_DOWN ? a : tl.g.base + tok;
+                    if (a >= 0) w.orow = tl.g.base + tok;
                     if (MODE == FP8_DOWN) {
                         if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                        else if (tl.rb == 0 && wg == 0) p.present[a] = 1;
+                        else if (tl.rb == 0 && wg == 0) p.z_row[a] = tl.g.base + tok + 1;
                     }
-                }
-            }
-            if (MODE == FP8_DENSE && p.residual && p.slices == 1 && w.orow >= 0 && w.it.kb1 == p.kb) {
-                // the thread's part of the residual's row into L2
-                const int es = p.y_bf16 ? 2 : 4;
-                const uint8_t* r = reinterpret_cast<const uint8_t*>(p.residual) + (size_t)w.orow * p.rows * es;
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int c = (2 * tl.rb + h) * kM + wg * 64;
-                    for (int o = 0; o < 64 * es; o += 128)
-                        if (c + o / es < p.rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + (size_t)c * es + o));
                 }
             }
             if (w.left > 0) fetch(w, w.it.kb0 & ~3);
@@ -475,6 +518,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             it = w.it;
 #pragma unroll
             for (int j = 0; j < C; j++) acc[j] = 0.0f;
+            // the residual of a whole tile is asked for a few steps into it, when the stores of
+            // the tile before have read the boxes
+            const int c0 = 2 * w.rb * kM + wg * 64;       // output columns: two runs of 64
+            bool ask = MODE == FP8_DENSE && p.boxed && p.residual && p.slices == 1 && left > 0;
+            auto ask_now = [&]() {
+                if (lane == 0) {
+                    if (p.y_bf16) ask_residual<__nv_bfloat16>(p, c0, w.y0, sm.box[warp][0], &sm.res[warp]);
+                    else ask_residual<float>(p, c0, w.y0, sm.box[warp][0], &sm.res[warp]);
+                }
+                __syncwarp();
+                ask = false;
+                asked++;
+            };
+            const bool whole = it.kb1 - it.kb0 == p.kb;
             if (left > 0) {
                 // scales of four K steps at a time, fetched four steps ahead
                 for (int kb = it.kb0 & ~3; kb < it.kb1; kb += 4) {
@@ -485,11 +542,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         sb[i] = xn[i] * bn[i];
                     }
                     if (kb + 4 < it.kb1) fetch(w, kb + 4);
+                    if constexpr (MODE == FP8_DENSE)
+                        if (ask && whole && kb > it.kb0) ask_now();
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         if (kb + i < it.kb0 || kb + i >= it.kb1) continue;
                         const int b = n % kBufs;
-                        if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                        if (!dead && !mbar_wait(&sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
                         tc_fence_after();
                         const uint32_t ta = lane_addr + (uint32_t)(b * 256 + wg * 64);
                         // loads run one chunk of 16 columns ahead of the arithmetic
@@ -513,13 +572,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // no token in this warp: only hand the buffers on
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int b = n % kBufs;
-                    if (!dead && !mbar_wait(&acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                    if (!dead && !mbar_wait(&sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
                     __syncwarp();
                     if (lane == 0) arrive_pair(ae + b * 8);
                 }
             }
             if (kAhead) more = look_up(next);
-            if (it.kb1 - it.kb0 < p.kb && p.slices == 1) {
+            if (!whole && p.slices == 1) {
                 // store the sums; the last part to arrive adds all of them up
                 const int o0 = sch.owner(it.tile * p.kb), o1 = sch.owner(it.tile * p.kb + p.kb - 1);
                 float4* dst = reinterpret_cast<float4*>(p.partial) +
@@ -531,9 +590,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 named_bar(1, kEpi);
-                if (tid == 0) flags[2] = arrive_last(&p.tickets[2 * o0 + rank], (uint32_t)(o1 - o0 + 1));
+                if (tid == 0) sm.last = arrive_last(&p.tickets[2 * o0 + rank], (uint32_t)(o1 - o0 + 1));
                 named_bar(1, kEpi);
-                if (!flags[2]) continue;
+                if (!sm.last) continue;
                 if (left > 0) {
 #pragma unroll
                     for (int j = 0; j < C; j++) acc[j] = 0.0f;
@@ -553,22 +612,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (MODE != FP8_GATE_UP) {
                 if (left <= 0) continue;
-                // output columns of the thread's two runs of 64
-                const int c0 = 2 * w.rb * kM + wg * 64;
-                const auto store = [&](auto* y, auto res) {
-                    using Y = std::remove_pointer_t<decltype(y)>;
-                    const Y* r = reinterpret_cast<const Y*>(p.residual);
-                    store_rows<Y, decltype(res)::value>(y, r, MODE == FP8_DENSE && p.slices > 1 ? p.pitch : p.rows, c0, w.orow,
-                                                        acc, stage, lane);
-                };
-                constexpr std::false_type none{};
-                constexpr std::true_type with{};
-                if (MODE == FP8_DOWN) store(p.z, none);
-                else if (p.slices > 1) store(p.partial + (size_t)it.slice * p.T * p.pitch, none);
-                else if (p.y_bf16 && p.residual) store(reinterpret_cast<__nv_bfloat16*>(p.y), with);
-                else if (p.y_bf16) store(reinterpret_cast<__nv_bfloat16*>(p.y), none);
-                else if (p.residual) store(reinterpret_cast<float*>(p.y), with);
-                else store(reinterpret_cast<float*>(p.y), none);
+                constexpr int NB = S::kBoxes > 0 ? S::kBoxes : 1;
+                float* plain = reinterpret_cast<float*>(sm.box[warp][0]);
+                if (MODE == FP8_DOWN) {
+                    // (H is a multiple of 64: a box has all of its columns)
+                    store_boxes<float, false, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane,
+                                                  left < 32 ? p.z : nullptr, left);
+                } else if (p.slices > 1) {
+                    store_boxes<float, false, NB>(&p.out, c0, w.y0, it.slice, p.pitch, acc, sm.box[warp][0], lane);
+                } else if (!p.boxed) {
+                    if (p.y_bf16)
+                        store_rows<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.y),
+                                                  reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.orow, acc,
+                                                  plain, lane);
+                    else
+                        store_rows<float>(reinterpret_cast<float*>(p.y), reinterpret_cast<const float*>(p.residual), p.rows, c0,
+                                          w.orow, acc, plain, lane);
+                } else if (p.residual) {
+                    if (ask) ask_now();
+                    if (!dead && !mbar_wait(&sm.res[warp], (asked - 1) & 1, p.status, kSite + 9)) dead = true;
+                    if (p.y_bf16) store_boxes<__nv_bfloat16, true, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane);
+                    else store_boxes<float, true, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane);
+                } else {
+                    if (p.y_bf16) store_boxes<__nv_bfloat16, false, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane);
+                    else store_boxes<float, false, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane);
+                }
             } else {
                 // SwiGLU of 64 columns; the scale block is this and the other warpgroup's
                 uint32_t top = 0;
@@ -579,9 +647,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         top = max(top, __float_as_uint(acc[j]) & 0x7FFFFFFFu);
                     }
                 }
-                tops[wg * kM + row] = top;
+                sm.top[wg][row] = top;
                 named_bar(1, kEpi);
-                top = max(top, tops[(wg ^ 1) * kM + row]);
+                top = max(top, sm.top[wg ^ 1][row]);
                 named_bar(1, kEpi);      // read before the next tile's
                 const Quantizer qz(top);
                 const int i0 = w.rb * kM + wg * 64;
@@ -601,6 +669,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        // this thread's stores are complete
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -614,9 +684,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int MODE>
 cudaError_t launch(const Params& p, int grid, cudaStream_t s)
 {
-    const cudaError_t e = allow_smem<fp8_pair_kernel<MODE>>(kSmem);
+    const cudaError_t e = allow_smem<fp8_pair_kernel<MODE>>(kSmem<MODE>);
     if (e != cudaSuccess) return e;
-    return launch_early<fp8_pair_kernel<MODE>>(grid, kThreads, kSmem, s, p);
+    return launch_early<fp8_pair_kernel<MODE>>(grid, kThreads, kSmem<MODE>, s, p);
 }
 
 }  // namespace

@@ -44,10 +44,10 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(int T, int N, int pitch, 
     }
 }
 
-// y[t] = residual[t] + z[T*k + t] (shared) + sum over slots of w[t][s] * z[t*k + s], in slot
+// y[t] = residual[t] + z[T*k + t] (shared) + sum over slots of w[t][s] * its row of z, in slot
 // order; slots that the lists leave out add nothing.
 __global__ void __launch_bounds__(256) fp8_combine_kernel(int T, int k, int H, int n_shared, const float* z,
-                                                          const uint8_t* present, const float* w,
+                                                          const int32_t* z_row, const float* w,
                                                           const float* residual, float* y)
 {
     pdl_launch_dependents();
@@ -66,10 +66,10 @@ __global__ void __launch_bounds__(256) fp8_combine_kernel(int T, int k, int H, i
             v.w += a.w;
         }
         for (int s = 0; s < k; s++) {
-            const size_t r = (size_t)t * k + s;
-            if (!present[r]) continue;
-            const float ws = w[r];
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(z) + r * h4 + c);
+            const int r = z_row[(size_t)t * k + s] - 1;
+            if (r < 0) continue;
+            const float ws = w[(size_t)t * k + s];
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(z) + (size_t)r * h4 + c);
             v.x = fmaf(ws, a.x, v.x);
             v.y = fmaf(ws, a.y, v.y);
             v.z = fmaf(ws, a.z, v.z);
@@ -121,6 +121,20 @@ bool weight_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uin
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Outputs [n][rows][cols] of es bytes a value, in boxes of 32 rows by 128 bytes.
+bool out_map(CUtensorMap* m, const void* base, int es, uint64_t cols, uint64_t rows, uint64_t n)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {cols, rows, n};
+    cuuint64_t strides[2] = {cols * es, cols * es * rows};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / es), 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool token_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, int box_rows)
 {
     auto enc = tensor_map_encoder();
@@ -150,7 +164,7 @@ size_t fp8_scratch_bytes(int mode, int64_t T, int H, int k, int n_shared)
 {
     size_t n = partial_bytes(T);
     if (mode == FP8_GATE_UP && T > kDecodeTokens) n += up((size_t)T * k * H);
-    if (mode == FP8_DOWN && T > kDecodeTokens) n += up((size_t)T * k) + up((size_t)T * (k + n_shared) * H * sizeof(float));
+    if (mode == FP8_DOWN && T > kDecodeTokens) n += up((size_t)T * k * 4) + up((size_t)T * (k + n_shared) * H * sizeof(float));
     return n;
 }
 
@@ -223,6 +237,12 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
             p.slices = most < 2 ? 1 : most < fit ? most : fit;
         }
         p.pitch = (a.N + 3) / 4 * 4;
+        const int es = a.y_bf16 && p.slices == 1 ? 2 : 4;
+        p.boxed = p.slices > 1 || a.N % (16 / es) == 0;
+        if (p.slices > 1) ok &= out_map(&p.out, p.partial, 4, p.pitch, a.T, p.slices);
+        else if (p.boxed) ok &= out_map(&p.out, a.y, es, a.N, a.T, 1);
+        if (p.boxed && p.slices == 1 && a.residual) ok &= out_map(&p.res, a.residual, es, a.N, a.T, 1);
+        if (!ok) return cudaErrorInvalidValue;
     }
     auto product = [&]() {
         return decode ? fp8_decode_launch(a.mode, p, a.num_sms, s) : fp8_pair_launch(a.mode, p, a.num_sms, s);
@@ -251,18 +271,19 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     }
     if (a.mode != FP8_DOWN || decode) return product();
     uint8_t* at = a.scratch + partial_bytes(a.T);
-    p.present = at;
-    p.z = reinterpret_cast<float*>(at + up((size_t)a.T * a.k));
-    const size_t words = up((size_t)a.T * a.k) / 16;
+    p.z_row = reinterpret_cast<int32_t*>(at);
+    p.z = reinterpret_cast<float*>(at + up((size_t)a.T * a.k * 4));
+    if (!out_map(&p.out, p.z, 4, a.H, (uint64_t)a.T * (a.k + a.n_shared), 1)) return cudaErrorInvalidValue;
+    const size_t words = up((size_t)a.T * a.k * 4) / 16;
     cudaError_t e = launch_early<fp8_clear_kernel>((int)((words + 255) / 256), 256, 0, s, words,
-                                                   reinterpret_cast<uint4*>(p.present));
+                                                   reinterpret_cast<uint4*>(p.z_row));
     if (e != cudaSuccess) return e;
     e = product();
     if (e != cudaSuccess) return e;
     const int64_t work = (int64_t)a.T * (a.H / 4);
     const int blocks = (int)(work + 255 < (int64_t)256 * a.num_sms * 8 ? (work + 255) / 256 : (int64_t)a.num_sms * 8);
     return launch_early<fp8_combine_kernel>(blocks, 256, 0, s, a.T, a.k, a.H, a.n_shared, (const float*)p.z,
-                                            (const uint8_t*)p.present, a.wts, reinterpret_cast<const float*>(a.residual),
+                                            (const int32_t*)p.z_row, a.wts, reinterpret_cast<const float*>(a.residual),
                                             reinterpret_cast<float*>(a.y));
 }
 

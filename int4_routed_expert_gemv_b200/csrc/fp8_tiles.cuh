@@ -19,6 +19,7 @@ constexpr int kMaxGroups = 1024 + 1;    // experts and the shared one
 // Parameters of a launch.
 struct Params {
     CUtensorMap w[2];             // dense or routed experts, shared expert
+    CUtensorMap out, res;         // above 16 tokens: y, slices or z, and the residual, 32 rows of 128 bytes
     CUtensorMap x[2];             // tokens; GATE_UP above 16 tokens: in list order, and as given
     int K, kb;                    // contraction length and its scale blocks
     int rows, rb;                 // output rows of a matrix, 256-row (or gate/up pair) blocks
@@ -36,8 +37,9 @@ struct Params {
     int y_bf16;
     uint8_t* hq;
     float* hs;
-    float* z;                     // DOWN: [T*k + T*n_shared][rows]
-    uint8_t* present;             // DOWN: [T*k] 1 where z has the row
+    float* z;                     // DOWN above 16 tokens: [T*k + T*n_shared][rows], in list order
+    int32_t* z_row;               // [T*k] 1 + row of z of t * k + slot, 0 where the lists leave it out
+    int boxed;                    // rows of the output begin on 16 bytes: out and res are set
     float* partial;               // sums of the parts of split tiles, or slices [slices][T][pitch]
     int slices, pitch;
     uint32_t* tickets;            // parts that have arrived, by the first part's worker
@@ -76,15 +78,16 @@ struct Group {
     int count;    // 0 where the lists are not a batch union's: nothing of them is read or written
 };
 
+template <int N>
 struct Groups {
-    int expert[kMaxGroups], base[kMaxGroups], count[kMaxGroups];
+    int expert[N], base[N], count[N];
     __device__ __forceinline__ Group at(int g) const { return Group{expert[g], base[g], count[g]}; }
 };
 
 // One warp: the groups of a launch into shared memory (loads that do not wait for one
 // another); returns how many there are.
-template <int MODE>
-__device__ __forceinline__ int read_groups(const Params& p, int lane, Groups& t)
+template <int MODE, int N>
+__device__ __forceinline__ int read_groups(const Params& p, int lane, Groups<N>& t)
 {
     int ng = 1;
     if (MODE != FP8_DENSE) {
@@ -193,7 +196,8 @@ struct Tile {
 };
 
 // first[g]: tiles of nt tokens before group g.
-__device__ __forceinline__ Tile tile_of(const Params& p, const Groups& t, const int* first, int n_groups, int nt, int tile)
+template <int N>
+__device__ __forceinline__ Tile tile_of(const Params& p, const Groups<N>& t, const int* first, int n_groups, int nt, int tile)
 {
     Tile v;
     const int q = tile / p.rb;
@@ -211,7 +215,8 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const Groups& t, const 
 }
 
 // One warp: first[] of every group; returns the tiles.
-__device__ __forceinline__ int plan_tiles(const Params& p, const Groups& t, int ng, int nt, int lane, int* first)
+template <int N>
+__device__ __forceinline__ int plan_tiles(const Params& p, const Groups<N>& t, int ng, int nt, int lane, int* first)
 {
     int base = 0;
     for (int g0 = 0; g0 < ng; g0 += 32) {
