@@ -11,8 +11,8 @@
 // weights there, the scales of all columns come from shared memory, and those reads, beside
 // the MMA's own, took 3 times as long as everything else.
 //
-// The tokens of an expert lie one after another: GATE_UP reads a copy in list order, made by
-// a launch before.  (Gathering tensor copies, four rows each, took 77 cycles a copy, 2500 a
+// The tokens of an expert lie one after another: GATE_UP reads a copy of rows and scales in list
+// order, made by a launch before.  (Gathering tensor copies, four rows each, took 77 cycles a copy, 2500 a
 // K step; cp.async by two warps 2000, as each hand-over to the MMA waits for the copies
 // behind it.)
 //
@@ -25,6 +25,8 @@
 //   warp 8      TMA producer of this CTA's tokens and weight rows
 //   warp 9      tensor memory; in rank 0, with warp 11, the pair's single-thread tcgen05.mma
 //               issuers, a K step each in turn
+//   warp 10     briefs: looks the next tiles up for the accumulating warps, whose time it would
+//               take (2500 cycles a tile)
 // A part of a split tile goes to the workspace; the last one to arrive adds the parts up in
 // K order (Schedule).
 #include <string.h>
@@ -59,6 +61,14 @@ struct Shape {
     static constexpr int kGroups = MODE == FP8_DENSE ? 1 : kMaxGroups;
 };
 
+// What the accumulating warps need to know of an item, looked up by a warp of its own.
+struct Brief {
+    Item it;                 // it.tile < 0: no more
+    int rb, expert, t0, n;   // row block, expert, first token of the group, tokens
+    int base;                // first row of the group
+};
+constexpr int kBriefs = 4;
+
 template <int MODE>
 struct Smem {
     using S = Shape<MODE>;
@@ -75,6 +85,8 @@ struct Smem {
     uint64_t acc_empty[kBufs];           // rank 0: read by every accumulating warp of the pair
     uint64_t mma_done[2];
     uint64_t res[kEpi / 32];             // a warp's part of the residual landed
+    uint64_t brief_full[kBriefs], brief_empty[kBriefs];
+    Brief brief[kBriefs];
 };
 template <int MODE>
 constexpr size_t kSmem = sizeof(Smem<MODE>) + 1024;
@@ -183,7 +195,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, 
 }
 
 // Until at most N of this thread's stores have still to read their boxes.
-template <int N>
+template <int N = 0>
 __device__ __forceinline__ void boxes_read()
 {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
@@ -201,7 +213,7 @@ struct Boxes {
 template <class Y>
 __device__ __forceinline__ void ask_residual(const Params& p, int c0, int y0, uint8_t* box, uint64_t* bar)
 {
-    boxes_read<0>();
+    boxes_read();
     uint32_t bytes = 0;
 #pragma unroll
     for (int j = 0; j < Boxes<Y>::N; j++) bytes += Boxes<Y>::column(c0, j) < p.rows ? kOutBox : 0;
@@ -280,7 +292,7 @@ __device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, in
                                            float* stage, int lane)
 {
     constexpr int P = 33;
-    if (lane == 0) boxes_read<0>();
+    if (lane == 0) boxes_read();
     __syncwarp();
 #pragma unroll
     for (int j0 = 0; j0 < C; j0 += 32) {
@@ -333,6 +345,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(&sm.mma_done[0], 1);
         mbar_init(&sm.mma_done[1], 1);
         for (int w = 0; w < kEpi / 32; w++) mbar_init(&sm.res[w], 1);
+        for (int b = 0; b < kBriefs; b++) {
+            mbar_init(&sm.brief_full[b], 1);
+            mbar_init(&sm.brief_empty[b], kEpi / 32);
+        }
         fence_barrier_init();
     }
     if (warp == 9) {
@@ -432,6 +448,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 commit_pair(&sm.mma_done[odd]);
                 mbar_wait(&sm.mma_done[odd], 0, p.status, kSite + 5);
             }
+        } else if (warp == 10) {
+            // ------------------------------- briefs -----------------------------------------
+            uint32_t m = 0;
+            for (bool more = true; more; m++) {
+                const int slot = m % kBriefs;
+                more = sch.next(it);
+                Tile tl{};
+                if (more) tl = tile_of(p, sm.groups, sm.first, n_groups, NT, it.tile);
+                if (!dead && !mbar_wait(&sm.brief_empty[slot], ((m / kBriefs) & 1) ^ 1, p.status, kSite + 11)) dead = true;
+                if (lane == 0) {
+                    if (!more) it.tile = -1;
+                    sm.brief[slot] = Brief{it, tl.rb, tl.g.expert, tl.t0, tl.n, tl.g.base};
+                    mbar_arrive(&sm.brief_full[slot]);
+                }
+                __syncwarp();
+                if (MODE == FP8_DOWN && more && tl.rb == 0 && it.kb0 == 0 && tl.g.expert >= 0)
+                    // where the combine finds the rows of z
+                    for (int j = rank * kM + lane; j < min(tl.n, (rank + 1) * kM); j += 32) {
+                        const int pos = tl.g.base + tl.t0 + j, a = position_of(p, pos);
+                        if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
+                        else p.z_row[a] = pos + 1;
+                    }
+            }
         }
     } else {
         // ------------------------- scaled accumulation, outputs -------------------------
@@ -440,12 +479,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int row = q * 32 + lane;              // token within the CTA's 128
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         float acc[C];
-        uint32_t asked = 0;                         // residual parts asked for
+        uint32_t asked = 0, briefs = 0;             // residual parts asked for, briefs read
         uint32_t n = 0;
         const uint32_t ae = map_to(&sm.acc_empty[0], 0);
         const int nb = fp8_blocks(p.rows);
-        // What a tile needs besides its sums.  The next tile's is looked up (list positions, then
-        // scales: loads that wait for one another) before this one's outputs are written.
+        // What a tile needs besides its sums.  The next tile's brief is taken, and its first scales
+        // are on their way, before this one's outputs are written.
         struct Work {
             Item it;
             int rb, expert, left;        // row block, expert, tokens of this warp
@@ -454,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         float xn[4], an[4], bn[4];       // scales of four K steps: token, both row blocks
         auto fetch = [&](const Work& w, int kb) {      // kb: a multiple of 4
-            const float* xs = p.xs + (size_t)w.xrow * p.kb;
+            const float* xs = (MODE == FP8_GATE_UP && w.expert < 0 ? p.xs_shared : p.xs) + (size_t)w.xrow * p.kb;
             const float* wa = w.expert < 0 ? p.ws[1]
                                            : reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws[0]) +
                                                                             (uint64_t)w.expert * p.ws_stride);
@@ -479,35 +518,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         };
         auto look_up = [&](Work& w) {
-            if (!sch.next(w.it)) return false;
-            const Tile tl = tile_of(p, sm.groups, sm.first, n_groups, NT, w.it.tile);
+            const int slot = briefs % kBriefs;
+            if (!dead && !mbar_wait(&sm.brief_full[slot], (briefs / kBriefs) & 1, p.status, kSite + 12)) dead = true;
+            const Brief tl = sm.brief[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.brief_empty[slot]);
+            briefs++;
+            if (dead || tl.it.tile < 0) return false;
+            w.it = tl.it;
             w.rb = tl.rb;
-            w.expert = tl.g.expert;
+            w.expert = tl.expert;
             w.left = tl.n - rank * kM - q * 32;
             const int tok = tl.t0 + rank * kM + row;            // token of the group
             w.xrow = 0;
             w.orow = -1;
-            w.y0 = (MODE == FP8_DENSE ? 0 : tl.g.base) + tok - lane;
+            w.y0 = (MODE == FP8_DENSE ? 0 : tl.base) + tok - lane;
             if (lane < w.left) {
                 if (MODE == FP8_DENSE) {
                     w.xrow = w.orow = tok;
-                } else if (tl.g.expert < 0) {
-                    w.xrow = MODE == FP8_DOWN ? tl.g.base + tok : tok;
-                    w.orow = tl.g.base + tok;
+                } else if (tl.expert < 0) {
+                    w.xrow = MODE == FP8_DOWN ? tl.base + tok : tok;
+                    w.orow = tl.base + tok;
                 } else {
-                    const int a = position_of(p, tl.g.base + tok);
-                    w.xrow = MODE == FP8_DOWN ? tl.g.base + tok : max(a, 0) / p.k;
-                    if (a >= 0) w.orow = tl.g.base + tok;
-                    if (MODE == FP8_DOWN) {
-                        if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                        else if (tl.rb == 0 && wg == 0) p.z_row[a] = tl.g.base + tok + 1;
-                    }
+                    w.xrow = w.orow = tl.base + tok;      // GATE_UP's scales are in list order too
                 }
             }
             if (w.left > 0) fetch(w, w.it.kb0 & ~3);
             return true;
         };
-        // (DENSE has no lists, and the registers are dear: there it is looked up when due.)
+        // (DENSE has more to write, and the registers are dear: there it is taken when due.)
         constexpr bool kAhead = MODE != FP8_DENSE;
         Work next;
         bool more = kAhead ? look_up(next) : true;

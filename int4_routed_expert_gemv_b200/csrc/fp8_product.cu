@@ -87,21 +87,27 @@ __global__ void __launch_bounds__(256) fp8_clear_kernel(size_t n, uint4* p)
     if (i < n) p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Rows of x in list order: row p is token assign[p] / k.  Positions that are none of the
-// batch's are flagged and leave their row as it is.
-__global__ void __launch_bounds__(256) fp8_gather_kernel(int positions, int k, int E, int pieces, const int32_t* n_union,
-                                                         const int32_t* offsets, const int32_t* assign, const uint4* x,
-                                                         uint4* to, uint32_t* status)
+// Rows of x and their scales in list order: row p is token assign[p] / k.  Positions that are none
+// of the batch's are flagged and get zeros.
+__global__ void __launch_bounds__(256) fp8_gather_kernel(int positions, int k, int E, int pieces, int kb,
+                                                         const int32_t* n_union, const int32_t* offsets,
+                                                         const int32_t* assign, const uint4* x, const float* xs, uint4* to,
+                                                         float* to_s, uint32_t* status)
 {
     pdl_launch_dependents();
     pdl_wait();
     const int nu = min(max(*n_union, 0), E);
-    const int64_t total = (int64_t)min(max(offsets[nu], 0), positions) * pieces;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int p = (int)(i / pieces), c = (int)(i - (int64_t)p * pieces);
+    const int rows = min(max(offsets[nu], 0), positions);
+    // a warp a row
+    const int warps = gridDim.x * 8, lane = threadIdx.x & 31;
+    for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < rows; p += warps) {
         const int a = assign[p];
-        if (a >= 0 && a < positions) to[i] = __ldg(x + (size_t)(a / k) * pieces + c);
-        else set_flag(status, DEV_BAD_INDEX);
+        const bool in = a >= 0 && a < positions;
+        const int t = in ? a / k : 0;
+        if (!in && lane == 0) set_flag(status, DEV_BAD_INDEX);
+        for (int c = lane; c < pieces; c += 32)
+            to[(size_t)p * pieces + c] = in ? __ldg(x + (size_t)t * pieces + c) : make_uint4(0, 0, 0, 0);
+        for (int c = lane; c < kb; c += 32) to_s[(size_t)p * kb + c] = in ? __ldg(xs + (size_t)t * kb + c) : 0.0f;
     }
 }
 
@@ -163,7 +169,7 @@ inline size_t partial_bytes(int64_t T)
 size_t fp8_scratch_bytes(int mode, int64_t T, int H, int k, int n_shared)
 {
     size_t n = partial_bytes(T);
-    if (mode == FP8_GATE_UP && T > kDecodeTokens) n += up((size_t)T * k * H);
+    if (mode == FP8_GATE_UP && T > kDecodeTokens) n += up((size_t)T * k * H) + up((size_t)T * k * fp8_blocks(H) * 4);
     if (mode == FP8_DOWN && T > kDecodeTokens) n += up((size_t)T * k * 4) + up((size_t)T * (k + n_shared) * H * sizeof(float));
     return n;
 }
@@ -248,11 +254,14 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
         return decode ? fp8_decode_launch(a.mode, p, a.num_sms, s) : fp8_pair_launch(a.mode, p, a.num_sms, s);
     };
     if (a.mode == FP8_GATE_UP && !decode) {
-        const int64_t pieces = (int64_t)a.T * a.k * (a.H / 16);
-        const int blocks = (int)(pieces + 255 < (int64_t)256 * a.num_sms * 8 ? (pieces + 255) / 256 : (int64_t)a.num_sms * 8);
-        const cudaError_t e = launch_early<fp8_gather_kernel>(blocks, 256, 0, s, a.T * a.k, a.k, a.E, a.H / 16, a.n_union,
-                                                              a.offsets, a.assign, reinterpret_cast<const uint4*>(a.x),
-                                                              reinterpret_cast<uint4*>(gathered), a.status);
+        const int64_t rows = (int64_t)a.T * a.k;
+        const int blocks = (int)(rows + 7 < (int64_t)8 * a.num_sms * 8 ? (rows + 7) / 8 : (int64_t)a.num_sms * 8);
+        float* scales = reinterpret_cast<float*>(gathered + up((size_t)rows * a.H));
+        p.xs = scales;
+        p.xs_shared = a.xs;
+        const cudaError_t e = launch_early<fp8_gather_kernel>(
+            blocks, 256, 0, s, a.T * a.k, a.k, a.E, a.H / 16, p.kb, a.n_union, a.offsets, a.assign,
+            reinterpret_cast<const uint4*>(a.x), a.xs, reinterpret_cast<uint4*>(gathered), scales, a.status);
         if (e != cudaSuccess) return e;
     }
     p.wts = a.wts;

@@ -26,7 +26,8 @@ struct Params {
     int T, k, E, n_shared, I;
     const float* ws[2];           // dense: scales; experts: first blob's scales, shared's
     uint64_t ws_stride;           // bytes between experts' scales
-    const float* xs;              // scales of the token codes
+    const float* xs;              // scales of the token codes (GATE_UP above 16 tokens: in list order)
+    const float* xs_shared;       // GATE_UP above 16 tokens: as given
     const float* wts;             // DOWN: routing weights
     const int32_t* union_ids;
     const int32_t* n_union;
