@@ -79,11 +79,6 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* m)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
-}
-
 // A run of K steps of one expert's matrix within an item.
 struct Segment {
     int g, rb;         // group, row block
@@ -154,6 +149,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
     if (warp == 9) tmem_alloc(&sm.tmem, kTmem);
     if (warp == 8 && lane < 3) prefetch_map(lane < 2 ? &p.w[lane] : &p.x[0]);
     pdl_launch_dependents();
+    if (MODE == FP8_DENSE && warp == 8 && lane == 0) {
+        // the first weights, while the kernel before ends
+        Schedule first;
+        Item f;
+        first.init(p.rb, p.kb, (int)gridDim.x, (int)blockIdx.x, kLeast, kJoin);
+        if (first.next(f))
+            for (int kb = f.kb0; kb < min(f.kb1, f.kb0 + kStages); kb++) {
+                prefetch_box(&p.w[0], kb * 128, f.tile * 2 * kM, 0);
+                prefetch_box(&p.w[0], kb * 128, f.tile * 2 * kM + kM, 0);
+            }
+    }
     pdl_wait();
     if (warp == 8) {
         const int ng = read_groups<MODE>(p, lane, sm.t.g);

@@ -93,6 +93,7 @@ template <bool BF16, int STEPS, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) fp8_norm_kernel(Fp8NormParams p)
 {
     __shared__ double part[32];
+    pdl_launch_dependents();      // a product that follows may fetch its first weights now
     const int nthr = blockDim.x, tid = threadIdx.x;
     const size_t row = (size_t)blockIdx.x * p.H;
     Piece<BF16> x[STEPS];

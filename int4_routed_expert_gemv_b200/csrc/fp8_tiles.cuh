@@ -264,6 +264,19 @@ __device__ __forceinline__ bool arrive_last(uint32_t* ticket, uint32_t parts)
     return last;
 }
 
+// A box of a 3-D map into L2.  Open before pdl_wait: L2 is where every SM's writes meet, so a line
+// fetched early is not stale later, as a copy into shared memory could be.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
 // Dynamic shared memory of a kernel, allowed once per kernel and device.
 template <auto Kernel>
 inline cudaError_t allow_smem(size_t bytes)
