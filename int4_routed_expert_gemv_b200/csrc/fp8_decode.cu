@@ -147,7 +147,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
         fence_barrier_init();
     }
     if (warp == 9) tmem_alloc(&sm.tmem, kTmem);
-    if (warp == 8 && lane < 3) prefetch_map(lane < 2 ? &p.w[lane] : &p.x[0]);
+    if (warp == 8 && lane == 0) {
+        prefetch_map(&p.w[0]);
+        prefetch_map(&p.x[0]);
+    }
     pdl_launch_dependents();
     if (MODE == FP8_DENSE && warp == 8 && lane == 0) {
         // the first weights, while the kernel before ends

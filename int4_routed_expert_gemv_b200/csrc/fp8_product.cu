@@ -6,8 +6,8 @@
 //   DENSE    y = round(residual + out)
 //   GATE_UP  row p of the union lists: h = silu(g) * u, then codes and scales of h
 //   DOWN     up to 16 tokens the combine is part of the product (fp8_decode.cu); above,
-//            z[t * k + slot] = out (fp32), and a second launch adds residual, the shared row and
-//            the routing-weighted rows of each token in a fixed order
+//            z = out (fp32, one row per position of the lists), and a second launch adds residual,
+//            the shared row and the routing-weighted rows of each token in a fixed order
 #include <string.h>
 
 #include "fp8_tiles.cuh"
@@ -164,6 +164,19 @@ inline size_t partial_bytes(int64_t T)
     return up((size_t)2 * kFp8Ctas * (T <= kDecodeTokens ? 16 : 128) * kEpi * sizeof(float));
 }
 
+// Batches above 16 tokens for which reading the weights counts more than the tensor rate: up to
+// so many tokens in all (DENSE), or rows of an expert on the average.  Both sides measured, us, with
+// fp8_mid.cu / fp8_pair.cu: dense 12288 x 6144, 64 tokens 24 / 34, 128 tokens 42 / 36; GLM-shaped
+// experts chosen evenly, gate/up of 32 rows 339 / 451, 48 rows 367 / 460, 64 rows 481 / 465 (unevenly, 50
+// rows 256 / 241, and at hidden 1024 32 rows 51 / 44); down of 64 rows 232 / 294, 96 rows 308 / 316, 128
+// rows 399 / 360.
+constexpr int kMidTokens = 64, kMidGateUp = 32, kMidDown = 80;
+
+bool mid_batch(int mode, int64_t T, int k, int E)
+{
+    return mode == FP8_DENSE ? T <= kMidTokens : T * k <= (int64_t)(mode == FP8_DOWN ? kMidDown : kMidGateUp) * E;
+}
+
 }  // namespace
 
 size_t fp8_scratch_bytes(int mode, int64_t T, int H, int k, int n_shared)
@@ -179,8 +192,9 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     Params p;
     memset(&p, 0, sizeof(p));
     const bool decode = a.T <= kDecodeTokens;
+    const bool mid = !decode && mid_batch(a.mode, a.T, a.k, a.E);
     // rows of a token box (1: rows gathered one by one)
-    const int box = !decode ? 128 : a.mode == FP8_DOWN ? 1 : 16;
+    const int box = mid ? 16 : !decode ? 128 : a.mode == FP8_DOWN ? 1 : 16;
     uint8_t* gathered = a.scratch + partial_bytes(a.T);
     bool ok = true;
     if (a.mode == FP8_DENSE) {
@@ -236,8 +250,8 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
         // Fewer tiles than half of the pairs: equal slices of K, at least 4 K steps each, and a
         // second launch that adds them up on every SM.  (Joining parts as the last one arrives
         // leaves that to one pair per tile: 77 x 576 x 6144 took 24 us so.)
-        const int pairs = (a.num_sms < kFp8Ctas ? a.num_sms : kFp8Ctas) / 2;
-        const int64_t tiles = (int64_t)((a.T + 255) / 256) * p.rb;
+        const int ctas = a.num_sms < kFp8Ctas ? a.num_sms : kFp8Ctas, pairs = mid ? ctas : ctas / 2;
+        const int64_t tiles = (int64_t)(mid ? (a.T + 63) / 64 : (a.T + 255) / 256) * p.rb;
         if (2 * tiles <= pairs) {
             const int most = p.kb / 4, fit = pairs / (int)tiles;
             p.slices = most < 2 ? 1 : most < fit ? most : fit;
@@ -245,13 +259,16 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
         p.pitch = (a.N + 3) / 4 * 4;
         const int es = a.y_bf16 && p.slices == 1 ? 2 : 4;
         p.boxed = p.slices > 1 || a.N % (16 / es) == 0;
-        if (p.slices > 1) ok &= out_map(&p.out, p.partial, 4, p.pitch, a.T, p.slices);
+        if (mid) p.boxed = 0;
+        else if (p.slices > 1) ok &= out_map(&p.out, p.partial, 4, p.pitch, a.T, p.slices);
         else if (p.boxed) ok &= out_map(&p.out, a.y, es, a.N, a.T, 1);
         if (p.boxed && p.slices == 1 && a.residual) ok &= out_map(&p.res, a.residual, es, a.N, a.T, 1);
         if (!ok) return cudaErrorInvalidValue;
     }
     auto product = [&]() {
-        return decode ? fp8_decode_launch(a.mode, p, a.num_sms, s) : fp8_pair_launch(a.mode, p, a.num_sms, s);
+        return decode ? fp8_decode_launch(a.mode, p, a.num_sms, s)
+               : mid  ? fp8_mid_launch(a.mode, p, a.num_sms, s)
+                      : fp8_pair_launch(a.mode, p, a.num_sms, s);
     };
     if (a.mode == FP8_GATE_UP && !decode) {
         const int64_t rows = (int64_t)a.T * a.k;

@@ -311,8 +311,9 @@ inline cudaError_t launch_early(int grid, int threads, size_t smem, cudaStream_t
 
 }  // namespace fp8
 
-// One launch of a product: for at most 16 tokens, and for more.
+// One launch of a product: for at most 16 tokens, for few more (or few per expert), for many.
 cudaError_t fp8_decode_launch(int mode, const fp8::Params& p, int num_sms, cudaStream_t s);
+cudaError_t fp8_mid_launch(int mode, const fp8::Params& p, int num_sms, cudaStream_t s);
 cudaError_t fp8_pair_launch(int mode, const fp8::Params& p, int num_sms, cudaStream_t s);
 
 }  // namespace coli

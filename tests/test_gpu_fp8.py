@@ -46,7 +46,7 @@ def run_matmul(T, N, K, dtype, residual, seed=0):
     return float(off.norm() / ref.norm())
 
 
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 77, 128, 129, 300])
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 64, 65, 77, 128, 129, 300])
 @pytest.mark.parametrize("N,K", [(1, 16), (64, 128), (129, 272), (576, 1024), (1000, 2064)])
 def test_matmul_sizes(colimoe, T, N, K):
     rel = run_matmul(T, N, K, torch.float32, residual=(T + N) % 2 == 0)
@@ -321,6 +321,15 @@ def test_gate_up(colimoe, H, I, E, k, ns, T):
 @pytest.mark.parametrize("T", [1, 4, 16, 17, 70, 200])
 def test_down(colimoe, H, I, E, k, ns, T):
     Case(H, I, E, k, ns, T, seed=T, hot=T % 2 == 0).check_down(residual=T % 3 != 0)
+
+
+@pytest.mark.parametrize("T", [100, 330])
+def test_many_rows_of_few_experts(colimoe, T):
+    # every kernel that a batch of experts can take: few rows per expert, some, many
+    for E in (3, 24):
+        c = Case(192, 320, E, 2, 1, T, seed=E)
+        c.check_gate_up()
+        c.check_down()
 
 
 def test_glm_shape(colimoe):
