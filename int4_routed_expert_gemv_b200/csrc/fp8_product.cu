@@ -29,13 +29,20 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(int T, int N, int pitch, 
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int t = (int)(i / n4), c = (int)(i - (int64_t)t * n4) * 4;
         float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-        for (int s = 0; s < slices; s++) {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(part) + (size_t)s * total + i);
-            f[0] += a.x;
-            f[1] += a.y;
-            f[2] += a.z;
-            f[3] += a.w;
+        // 16 slices' loads under way together: 4 at a time took 2.5 us longer over 12 slices
+        for (int s0 = 0; s0 < slices; s0 += 16) {
+            float4 a[16];
+#pragma unroll
+            for (int j = 0; j < 16; j++)
+                a[j] = s0 + j < slices ? __ldcs(reinterpret_cast<const float4*>(part) + (size_t)(s0 + j) * total + i)
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                f[0] += a[j].x;
+                f[1] += a[j].y;
+                f[2] += a[j].z;
+                f[3] += a[j].w;
+            }
         }
         const size_t o = (size_t)t * N + c;
 #pragma unroll
@@ -65,15 +72,27 @@ __global__ void __launch_bounds__(256) fp8_combine_kernel(int T, int k, int H, i
             v.z += a.z;
             v.w += a.w;
         }
-        for (int s = 0; s < k; s++) {
-            const int r = z_row[(size_t)t * k + s] - 1;
-            if (r < 0) continue;
-            const float ws = w[(size_t)t * k + s];
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(z) + (size_t)r * h4 + c);
-            v.x = fmaf(ws, a.x, v.x);
-            v.y = fmaf(ws, a.y, v.y);
-            v.z = fmaf(ws, a.z, v.z);
-            v.w = fmaf(ws, a.w, v.w);
+        // 4 slots' loads under way together
+        for (int s0 = 0; s0 < k; s0 += 4) {
+            float4 a[4];
+            float ws[4];
+            int r[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                r[j] = s0 + j < k ? z_row[(size_t)t * k + s0 + j] - 1 : -1;
+                ws[j] = s0 + j < k ? w[(size_t)t * k + s0 + j] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (r[j] >= 0) a[j] = __ldcs(reinterpret_cast<const float4*>(z) + (size_t)r[j] * h4 + c);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (r[j] < 0) continue;
+                v.x = fmaf(ws[j], a[j].x, v.x);
+                v.y = fmaf(ws[j], a[j].y, v.y);
+                v.z = fmaf(ws[j], a[j].z, v.z);
+                v.w = fmaf(ws[j], a[j].w, v.w);
+            }
         }
         reinterpret_cast<float4*>(y)[i] = v;
     }
