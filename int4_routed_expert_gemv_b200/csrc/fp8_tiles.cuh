@@ -241,16 +241,21 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// silu(g) * u.  The quotient g / (1 + exp(-g)) is an approximate reciprocal's with one correction
-// by its remainder (as Quantizer's), so it is off by little more than its rounding; where the
-// denominator is so large that the reciprocal could underflow, the quotient is 0 to within the
-// smallest normal number (and NaN for g = -inf, like -inf / inf).
+// silu(g) * u = g * u / (1 + e^-g).  e^-g is 2^t, t = -g / ln 2 rounded, times 1 + c, where
+// c = -g - t ln 2 is what the rounding of t left out (one FMA, nearly exact, as its terms nearly cancel; c^2 is
+// far below a rounding).  The quotient is an approximate reciprocal's with one correction by its
+// remainder, as Quantizer's.  With g held to -88 the denominator stays finite, and from 2^126 on its
+// reciprocal is flushed to 0, which the quotient is to within 2^-119.
 __device__ __forceinline__ float swiglu(float g, float u)
 {
-    const float d = 1.0f + expf(-g);
-    const float r = __fdividef(1.0f, d), q = g * r;
-    const float s = d >= 0x1p120f ? g * 0.0f : fmaf(fmaf(-q, d, g), r, q);
-    return s * u;
+    const float x = fminf(fmaxf(g, -88.0f), 200.0f);
+    const float t = x * -1.44269504f, c = fmaf(t, -0.693147181f, -x);
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    const float d = 1.0f + fmaf(e, c, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    const float q = g * r;
+    return fmaf(fmaf(-q, d, g), r, q) * u;
 }
 
 // One thread, after its CTA's barrier: counts a part of a tile whose sums the CTA has stored.

@@ -18,6 +18,13 @@ def product_bound(kb: int, more: int = 0) -> float:
     return 128 * 2 * U32 + (kb + 3 + more) * U32
 
 
+# silu(g) * u, relative, in half steps of fp32: 4 for the power of two (2^-22), 1 for its product
+# with 1 + c, |g| / 20 for ln 2 as a float in c (off by 1.9e-9, times |g| / ln 2), 1 each for 1 + e^-g, the
+# corrected quotient and the product with u.
+def silu_bound(g: torch.Tensor) -> torch.Tensor:
+    return (8 + g.abs() / 20) * U32 * (1 + 2.0 ** -16)
+
+
 def blocks(n: int) -> int:
     return (n + 127) // 128
 
@@ -133,8 +140,8 @@ def gate_up(L: Layer, xq, xs, lst):
         dg, du = rel * (xe.abs() @ G.abs().T), rel * (xe.abs() @ U.abs().T)
         s = ge * torch.sigmoid(ge)
         h[at] = s * ue
-        # |silu'| <= 1.1; exp, the quotient and the product: 8 roundings of fp32 at most
-        err[at] = 1.1 * ue.abs() * dg + s.abs() * du + 1.1 * dg * du + 8 * U32 * (s * ue).abs()
+        # |silu'| <= 1.1; the rest as silu_bound has it
+        err[at] = 1.1 * ue.abs() * dg + s.abs() * du + 1.1 * dg * du + silu_bound(ge) * (s * ue).abs()
         named[at] = True
     return h, err, named
 

@@ -218,9 +218,62 @@ def test_norm_zero_and_non_finite_rows(colimoe):
     check_norm(x[4:], None, None, 1e-6, None, out[4:], q[4:].view(R.E4M3), s[4:])
 
 
+def test_norm_codes_at_every_scale(colimoe):
+    # 21 blocks whose values lie around 2^-149 .. 2^127, one of them with values far below its largest
+    exps = [-149, -140, -126, -120, -101, -100, -99, -92, -91, -90, -89, -82, -10, 0, 82, 89, 98, 99, 100, 110, 125]
+    H = 128 * len(exps)
+    g = torch.Generator().manual_seed(3)
+    gamma = torch.ldexp(torch.ones(H), torch.tensor(exps).repeat_interleave(128))
+    x = torch.randn(4, H, generator=g)
+    x[1] = x[1] * torch.exp(-4 * torch.rand(H, generator=g) ** 2 * 6)
+    x[2, ::2] = 0
+    x = x.clamp(-3.9, 3.9)
+    q, s = torch.empty(4, H, dtype=torch.uint8, device="cuda"), torch.empty(4, len(exps), device="cuda")
+    out = torch.empty(4, H, device="cuda")
+    B.check(B.coli_rmsnorm_fp8(H, 4, x.cuda(), None, gamma.cuda(), 1e-6, None, out, q, s))
+    n, s = out.cpu(), s.cpu()
+    top = n.double().abs().view(4, -1, 128).amax(2) / 448
+    assert torch.equal(s, top.float())
+    want = torch.where(s[:, :, None] > 0, n.view(4, -1, 128).double() / s[:, :, None].double(), 0.0).float()
+    want = want.clamp(-448, 448).view(4, H).to(R.E4M3).view(torch.uint8)
+    same = (q.cpu() == want) | ((q.cpu() | want) & 0x7F == 0)
+    assert same.all(), (~same).nonzero()[:8]
+
+
 # ------------------------------------------------------------------------------------------------
 # experts
 # ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("T", [16, 60, 400])
+def test_swiglu_over_its_range(colimoe, T):
+    # one column of h: g = u = +-xs, so its scale is silu(g) * g / 448 with all of fp32
+    H, I = 128, 64
+    v = torch.cat([torch.linspace(-79, 200, T - 8), torch.tensor([0.0, 1e-30, -1e-30, 1e-3, -1e-3, 1e4, -1e4, -95.0])])
+    x = torch.zeros(T, H, dtype=torch.uint8)
+    x[:, 0] = torch.where(v < 0, 0xB8, 0x38).to(torch.uint8)               # e4m3 -1 and 1
+    one = torch.zeros(I, H, dtype=torch.uint8)
+    one[0, 0] = 0x38
+    blob = torch.cat([one.reshape(-1), one.reshape(-1), torch.zeros(H * I, dtype=torch.uint8),
+                      torch.ones(3).view(torch.uint8)])
+    stride = (blob.numel() + 255) // 256 * 256
+    experts = torch.zeros(2, stride, dtype=torch.uint8)
+    experts[0, :blob.numel()] = blob
+    experts = experts.cuda()
+    dims, weights = B.make_dims(H, I, 2, 1, 0), B.make_weights(None, None, experts, None, stride)
+    lst = [t.cuda() for t in R.lists(torch.zeros(T, 1, dtype=torch.int32), 2)]
+    ws = torch.zeros(B.coli_moe_workspace_bytes_fp8(dims, T), dtype=torch.uint8, device="cuda")
+    B.check(B.coli_moe_workspace_init(ws))
+    hq, hs = torch.empty(T, I, dtype=torch.uint8, device="cuda"), torch.empty(T, 1, device="cuda")
+    B.check(B.coli_moe_gate_up_fp8(dims, weights, x.cuda(), v.abs()[:, None].cuda(), T, *lst, hq, hs, ws))
+    assert B.coli_moe_read_status(ws) == (B.COLI_OK, 0)
+    g = v.double()
+    h = g * torch.sigmoid(g) * g
+    got = hs.cpu()[:, 0].double() * 448
+    # beside silu_bound one rounding for the scale; below 2^-126 and at g = -95 the smallest normal number counts
+    off = (got - h.abs()).abs()
+    bound = h.abs() * (R.silu_bound(g) + R.U32) + 448 * 2.0 ** -126
+    assert (off <= bound).all(), (float((off / bound).max()), float(v[(off / bound).argmax()]))
+
+
 class Case:
     """A layer on the device with lists, outputs and a workspace."""
 
