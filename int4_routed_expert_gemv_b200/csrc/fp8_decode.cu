@@ -20,7 +20,7 @@
 //   warp 8      TMA producer: weight tiles (3-D map over all experts) and token rows
 //   warp 9      TMEM allocator and single-thread tcgen05.mma issuer
 //   warp 10     products of token and weight scales of each K step, into a ring
-//   warp 11     idle
+//   warp 11     checks of the lists
 //
 // Work is cut into (tile, K step) units (Schedule).  A CTA with a part of a tile writes its
 // sums to the workspace and the last one to arrive adds the parts up in K order, so nothing
@@ -445,11 +445,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                 named_bar(2 + wg, 128);      // the maxima are read before the next tile's
             }
         }
-        // list positions that are none of the batch's
-        if (MODE != FP8_DENSE && blockIdx.x == 0)
-            for (int g = p.n_shared; g < ng; g++)
-                for (int l = tid; l < sm.t.g.count[g]; l += kEpi)
-                    if (sm.t.pos[sm.t.g.base[g] + l] < 0) set_flag(p.status, DEV_BAD_INDEX);
+    } else if (MODE != FP8_DENSE && blockIdx.x == 0) {
+        // warp 11: list positions that are none of the batch's, or whose token the list names again
+        bool bad = false;
+        for (int g = p.n_shared + lane; g < ng; g += 32) {
+            const int count = sm.t.g.count[g], base = sm.t.g.base[g];
+            bad |= count > p.T;
+            for (int l = 0; l < min(count, p.T); l++) {
+                const int a = sm.t.pos[base + l];
+                bad |= a < 0;
+                for (int i = l + 1; i < min(count, p.T); i++) bad |= a / p.k == sm.t.pos[base + i] / p.k;
+            }
+        }
+        if (bad) set_flag(p.status, DEV_BAD_INDEX);
     }
     tc_fence_before();
     __syncthreads();

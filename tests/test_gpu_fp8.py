@@ -437,6 +437,58 @@ def test_bad_lists_are_flagged_and_not_followed(colimoe):
             assert st == (B.COLI_EDEVICE, B.DEV_BAD_INDEX), (bad, st)
 
 
+def test_a_token_twice_in_a_list(colimoe):
+    # up to 16 tokens it is flagged (coli_moe_union flags the routing already); above, every position counts
+    for T in (3, 40):
+        c = Case(256, 192, 6, 2, 1, T, seed=8)
+        c.idx[1] = c.idx[1, 0]
+        c.lst = R.lists(c.idx, 6)
+        c.dl = [t.cuda() for t in c.lst]
+        if T > 16:
+            c.check_gate_up()
+            c.check_down()
+            continue
+        hq, hs = R.activations(c.rows, 192, torch.Generator().manual_seed(1))
+        for call in (lambda: B.coli_moe_gate_up_fp8(c.dims, c.weights, c.xq.cuda(), c.xs.cuda(), T, *c.dl, c.hq, c.hs, c.ws),
+                     lambda: B.coli_moe_down_fp8(c.dims, c.weights, hq.cuda(), hs.cuda(), T, c.w.cuda(), *c.dl, None, c.y,
+                                                 c.ws)):
+            B.check(B.coli_moe_workspace_init(c.ws))
+            B.check(call())
+            assert B.coli_moe_read_status(c.ws) == (B.COLI_EDEVICE, B.DEV_BAD_INDEX)
+
+
+@pytest.mark.parametrize("T", [3, 40, 150])
+def test_two_graphs_share_a_workspace(colimoe, T):
+    # replayed in turn on one stream: one's counters and parts are done with when the other begins
+    c = Case(512, 256, 6, 2, 1, T, seed=9)
+    g = torch.Generator().manual_seed(10)
+    hq, hs = (t.cuda() for t in R.activations(c.rows, 256, g))
+    w, res, xq, xs = c.w.cuda(), c.res.cuda(), c.xq.cuda(), c.xs.cuda()
+
+    def up():
+        B.check(B.coli_moe_gate_up_fp8(c.dims, c.weights, xq, xs, T, *c.dl, c.hq, c.hs, c.ws))
+
+    def down():
+        B.check(B.coli_moe_down_fp8(c.dims, c.weights, hq, hs, T, w, *c.dl, res, c.y, c.ws))
+
+    up()
+    down()
+    want = c.hq.clone(), c.hs.clone(), c.y.clone()
+    graphs = []
+    for f in (up, down):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f()
+    for _ in range(3):
+        c.hq[:c.rows] = 0
+        c.hs[:c.rows] = 0
+        c.y[:T] = 0
+        graphs[0].replay()
+        graphs[1].replay()
+        assert torch.equal(c.hq, want[0]) and torch.equal(c.hs, want[1]) and torch.equal(c.y[:T], want[2][:T])
+    assert B.coli_moe_read_status(c.ws) == (B.COLI_OK, 0)
+
+
 # ------------------------------------------------------------------------------------------------
 # together
 # ------------------------------------------------------------------------------------------------
