@@ -284,36 +284,60 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap* map, int c0, int 
     }
 }
 
-// The same without boxes, for rows that do not begin on 16 bytes and for a warp whose rows end
-// inside it (orow: a thread's row of y, -1 for none): 32 columns at a time go through shared
-// memory, so that a warp writes 32 consecutive values of a row.
+// A warp's part of the residual on its way into L2: a lane a row, two runs of 64 columns.
 template <class Y>
-__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int orow, const float (&acc)[C],
+__device__ __forceinline__ void prefetch_rows(const Y* residual, int rows, int c0, int y0, int left, int lane)
+{
+    if (lane >= left) return;
+#pragma unroll
+    for (int run = 0; run < 2; run++) {
+        const int last = min(64, rows - c0 - run * kM) - 1;
+        if (last < 0) break;
+        const Y* at = residual + (size_t)(y0 + lane) * rows + c0 + run * kM;
+#pragma unroll
+        for (int j = 0; j <= 64; j += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + min(j, last)));
+    }
+}
+
+// The same without boxes, for rows that do not begin on 16 bytes (the first `left` rows from y0):
+// 32 columns at a time go through shared memory, so that a warp writes 32 consecutive values of a
+// row.  The residual is in L2 by then: read from HBM here, it took 4000 x 4002 x 2048 in
+// fp32 from 70 us without one to 164; so it takes 95.  (Pieces of 16 bytes that begin where memory does,
+// 256 columns a row, took 79 without one and 113 with it.)
+template <class Y>
+__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int y0, int left, const float (&acc)[C],
                                            float* stage, int lane)
 {
-    constexpr int P = 33;
+    constexpr int P = 33, B = 16;      // rows whose loads are under way together
     if (lane == 0) boxes_read();
-    __syncwarp();
 #pragma unroll
     for (int j0 = 0; j0 < C; j0 += 32) {
         const int col = c0 + (j0 >> 6) * kM + (j0 & 63) + lane;
-        const bool in = col < rows;
+        const int n = col < rows ? left : 0;
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 32; j++) stage[lane * P + j] = acc[j0 + j];
         __syncwarp();
-        for (int r0 = 0; r0 < 32; r0 += 8) {
-            float v[8];
-            size_t at[8];
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += B) {
+            const size_t at = (size_t)(y0 + r0) * rows + col;
+            // (nothing but the loads and the stores under a condition: a branch around more of it would
+            // make the rows wait for one another)
+            Y v[B];
+            float f[B];
 #pragma unroll
-            for (int r = 0; r < 8; r++) {
-                const int to = __shfl_sync(0xffffffffu, orow, r0 + r);
-                at[r] = to >= 0 && in ? (size_t)to * rows + col : ~(size_t)0;
-                v[r] = stage[(r0 + r) * P + lane] + (residual && at[r] != ~(size_t)0 ? (float)residual[at[r]] : 0.0f);
+            for (int r = 0; r < B; r++)
+                if (residual && r0 + r < n) v[r] = residual[at + (size_t)r * rows];
+#pragma unroll
+            for (int r = 0; r < B; r++) f[r] = stage[(r0 + r) * P + lane];
+            if (residual) {
+#pragma unroll
+                for (int r = 0; r < B; r++) f[r] += (float)v[r];
             }
 #pragma unroll
-            for (int r = 0; r < 8; r++)
-                if (at[r] != ~(size_t)0) y[at[r]] = (Y)v[r];
+            for (int r = 0; r < B; r++)
+                if (r0 + r < n) y[at + (size_t)r * rows] = (Y)f[r];
         }
     }
     __syncwarp();
@@ -571,6 +595,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 asked++;
             };
             const bool whole = it.kb1 - it.kb0 == p.kb;
+            if (MODE == FP8_DENSE && !p.boxed && p.residual) {
+                if (p.y_bf16) prefetch_rows(reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.y0, left, lane);
+                else prefetch_rows(reinterpret_cast<const float*>(p.residual), p.rows, c0, w.y0, left, lane);
+            }
             if (left > 0) {
                 // scales of four K steps at a time, fetched four steps ahead
                 for (int kb = it.kb0 & ~3; kb < it.kb1; kb += 4) {
@@ -662,11 +690,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 } else if (!p.boxed) {
                     if (p.y_bf16)
                         store_rows<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.y),
-                                                  reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.orow, acc,
+                                                  reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.y0, left, acc,
                                                   plain, lane);
                     else
                         store_rows<float>(reinterpret_cast<float*>(p.y), reinterpret_cast<const float*>(p.residual), p.rows, c0,
-                                          w.orow, acc, plain, lane);
+                                          w.y0, left, acc, plain, lane);
                 } else if (p.residual) {
                     if (ask) ask_now();
                     if (!dead && !mbar_wait(&sm.res[warp], (asked - 1) & 1, p.status, kSite + 9)) dead = true;
