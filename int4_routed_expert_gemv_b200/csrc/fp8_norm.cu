@@ -22,10 +22,6 @@ namespace {
 
 using fp8::bf16x2_bits;
 
-struct Row8 {
-    float v[8];
-};
-
 // 8 columns as they are kept: fp32, or bf16 pairs.
 template <bool BF16>
 struct Piece {
@@ -74,17 +70,25 @@ struct Piece {
     }
 };
 
-// v * g * r rounded once, r = rh + rl: the product as a sum of two floats each (FMA gives the
-// products' remainders), which is off by less than 2^-44 before the rounding; where something
-// could underflow or is not finite, in double.
-__device__ __forceinline__ float scaled(float v, float g, double r, float rh, float rl)
+// n = v * g * r of 8 columns, each rounded once, r = rh + rl: the product as a sum of two floats
+// (FMA gives the products' remainders), which is off by less than 2^-44 before the rounding;
+// where something could underflow or is not finite, in double.  One test for all 8: a branch per
+// column took 8192 x 6144 in bf16 from 94 to 105 us, where instructions are what bounds.
+__device__ __forceinline__ void scaled(float (&n)[8], const float (&v)[8], const float (&g)[8], double r, float rh, float rl)
 {
-    const float p = v * g, e = fmaf(v, g, -p);
-    const float hi = p * rh;
-    const float lo = fmaf(e, rh, fmaf(p, rl, fmaf(p, rh, -hi)));
-    const float n = hi + lo;
-    if (fabsf(p) > 0x1p-90f && fabsf(hi) > 0x1p-90f && fabsf(hi) < 0x1p90f && rh < 0x1p90f && rh > 0x1p-60f) return n;
-    return (float)((double)v * (double)g * r);
+    float least = 1.0f, most = 1.0f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float p = v[j] * g[j], e = fmaf(v[j], g[j], -p);
+        const float hi = p * rh;
+        n[j] = hi + fmaf(e, rh, fmaf(p, rl, fmaf(p, rh, -hi)));
+        least = fminf(least, fminf(fabsf(p), fabsf(hi)));
+        most = fmaxf(most, fabsf(hi));
+    }
+    // (NaN, which the comparisons pass over, is NaN either way)
+    if (least > 0x1p-90f && most < 0x1p90f && rh < 0x1p90f && rh > 0x1p-60f) return;
+#pragma unroll
+    for (int j = 0; j < 8; j++) n[j] = (float)((double)v[j] * (double)g[j] * r);
 }
 
 // One CTA per row, blockDim.x a multiple of 32, STEPS * blockDim.x * 8 >= H.  x may alias
@@ -140,24 +144,29 @@ __global__ void __launch_bounds__(THREADS, CTAS) fp8_norm_kernel(Fp8NormParams p
         const bool in = c < p.H;
         Piece<false> g;
         if (p.gamma && in) g.load(p.gamma, c);
-        Row8 n;
+        float n[8], v[8], gs[8];
         uint32_t top = 0;      // bits of the largest |n|; a NaN's bits are above every number's
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            n.v[j] = in ? scaled(x[i].at(j), p.gamma ? g.at(j) : 1.0f, r, rh, rl) : 0.0f;
-            top = max(top, __float_as_uint(n.v[j]) & 0x7FFFFFFFu);
+            v[j] = x[i].at(j);
+            gs[j] = p.gamma ? g.at(j) : 1.0f;
+        }
+        if (in) {
+            scaled(n, v, gs, r, rh, rl);
+#pragma unroll
+            for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(n[j]) & 0x7FFFFFFFu);
         }
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (!in) continue;
         if (p.out) {
             float4* f = reinterpret_cast<float4*>(p.out + row + c);
-            f[0] = make_float4(n.v[0], n.v[1], n.v[2], n.v[3]);
-            f[1] = make_float4(n.v[4], n.v[5], n.v[6], n.v[7]);
+            f[0] = make_float4(n[0], n[1], n[2], n[3]);
+            f[1] = make_float4(n[4], n[5], n[6], n[7]);
         }
         const Quantizer qz(top);
-        const uint32_t lo = qz.codes(n.v[0], n.v[1]) | qz.codes(n.v[2], n.v[3]) << 16;
-        const uint32_t hi = qz.codes(n.v[4], n.v[5]) | qz.codes(n.v[6], n.v[7]) << 16;
+        const uint32_t lo = qz.codes(n[0], n[1]) | qz.codes(n[2], n[3]) << 16;
+        const uint32_t hi = qz.codes(n[4], n[5]) | qz.codes(n[6], n[7]) << 16;
         *reinterpret_cast<uint2*>(p.q + row + c) = make_uint2(lo, hi);
         if ((tid & 15) == 0) p.scales[(size_t)blockIdx.x * nb + c / kFp8Block] = qz.scale;
     }
@@ -168,13 +177,14 @@ cudaError_t launch(const Fp8NormParams& p, int num_sms, cudaStream_t s)
 {
     const int chunks = (p.H + 7) / 8;                 // 8-column pieces of a row
     // With few rows a piece a thread, for the shortest way through a row.  With many, up to
-    // four pieces a thread and about 256 threads, so that five rows are on an SM and one's loads
-    // run beside another's reduction (8192 x 6144 bf16: 3 pieces 106 us, 2 pieces 110, 4 pieces
-    // 130, 1 piece 128; six rows an SM spill, 118).
+    // four pieces a thread and about 256 threads, so that four or five rows are on an SM and one's
+    // loads run beside another's reduction.  8192 x 6144 with residual and out, three pieces: four rows
+    // an SM 91 us in bf16 (6.1 TB/s), 132 in fp32 (6.5 TB/s); five, which spill, 94 and 142.  4096 x 8192,
+    // four pieces, bf16 residual: four rows 56 us, three 60, five 58.
     auto threads = [&](int steps) { return ((chunks + steps - 1) / steps + 31) / 32 * 32; };
     const int many = p.T > 2 * num_sms ? (chunks + 255) / 256 : 0;
     if (many == 2) fp8_norm_kernel<BF16, 2, 256, 5><<<p.T, threads(2), 0, s>>>(p);
-    else if (many == 3) fp8_norm_kernel<BF16, 3, 256, 5><<<p.T, threads(3), 0, s>>>(p);
+    else if (many == 3) fp8_norm_kernel<BF16, 3, 256, 4><<<p.T, threads(3), 0, s>>>(p);
     else if (many == 4) fp8_norm_kernel<BF16, 4, 256, 4><<<p.T, threads(4), 0, s>>>(p);
     else if (chunks <= 768) fp8_norm_kernel<BF16, 1, 768, 1><<<p.T, threads(1), 0, s>>>(p);
     else if (chunks <= 1536) fp8_norm_kernel<BF16, 2, 768, 1><<<p.T, threads(2), 0, s>>>(p);
