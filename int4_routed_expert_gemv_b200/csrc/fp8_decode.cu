@@ -25,6 +25,12 @@
 // Work is cut into (tile, K step) units (Schedule).  A CTA with a part of a tile writes its
 // sums to the workspace and the last one to arrive adds the parts up in K order, so nothing
 // waits and results do not depend on the order of arrival.
+//
+// Bounded by reading the weights from HBM, and below some 100 MB by what a launch takes before the
+// first tile lands and after the last (lists, barriers, the first copies: 4 us; joining parts: 3 us).  Measured
+// back to back: GLM-shaped gate/up of one token 40 us (5.6 TB/s; no tile is split), of 16 tokens 136 us
+// (6.3 TB/s); down of one token 29 us (3.9 TB/s, every tile in 6 to 8 parts), of 16 79 us (5.4 TB/s); dense
+// 1 x 12288 x 6144 19 us (4.0 TB/s).
 #include <string.h>
 
 #include "fp8_tiles.cuh"
