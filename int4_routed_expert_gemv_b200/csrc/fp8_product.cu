@@ -196,6 +196,11 @@ bool mid_batch(int mode, int64_t T, int k, int E)
     return mode == FP8_DENSE ? T <= kMidTokens : T * k <= (int64_t)(mode == FP8_DOWN ? kMidDown : kMidGateUp) * E;
 }
 
+// Output rows that do not begin on 16 bytes leave the pairs slowly, which few K steps do not hide.  fp8_mid.cu /
+// fp8_pair.cu, us: 543 x 7298 x 208 to bf16 14 / 22, onto a residual 20 / 31; 187 x 2259 x 320 8.7 / 12.3; 725 x 3846
+// x 272 onto a residual 21.0 / 19.8; 4000 x 4001 x 512 onto a residual 68 / 67, x 1024 63 / 52.
+constexpr int kMidCols = 3 * kFp8Block;
+
 }  // namespace
 
 size_t fp8_scratch_bytes(int mode, int64_t T, int H, int k, int n_shared)
@@ -211,7 +216,8 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     Params p;
     memset(&p, 0, sizeof(p));
     const bool decode = a.T <= kDecodeTokens;
-    const bool mid = !decode && mid_batch(a.mode, a.T, a.k, a.E);
+    const bool ragged = a.mode == FP8_DENSE && a.N % (a.y_bf16 ? 8 : 4) != 0;
+    const bool mid = !decode && (mid_batch(a.mode, a.T, a.k, a.E) || (ragged && a.K <= kMidCols));
     // rows of a token box (1: rows gathered one by one)
     const int box = mid ? 16 : !decode ? 128 : a.mode == FP8_DOWN ? 1 : 16;
     uint8_t* gathered = a.scratch + partial_bytes(a.T);

@@ -59,6 +59,14 @@ def test_matmul_bf16(colimoe, T, N, K, residual):
     run_matmul(T, N, K, torch.bfloat16, residual)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,N,K", [(300, 5001, 640), (600, 4902, 400), (600, 5003, 272), (257, 5185, 16)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_matmul_rows_of_any_length(colimoe, dtype, T, N, K, residual):
+    # rows of y that do not begin on 16 bytes, of many tiles, whole and split, with many and with few K steps
+    run_matmul(T, N, K, dtype, residual)
+
+
 def test_matmul_many_tiles(colimoe):
     # more tiles than CTAs, so whole tiles and split ones in one launch
     for T, N, K in [(1024, 6144, 256), (2049, 4100, 128)]:
@@ -96,15 +104,15 @@ def test_matmul_more_than_32_bits_of_outputs(colimoe):
 
 def test_matmul_in_place_residual(colimoe):
     g = torch.Generator().manual_seed(4)
-    T, N, K = 33, 257, 512
-    xq, xs = (t.cuda() for t in R.activations(T, K, g))
-    wq, s = (t.cuda() for t in R.weights(N, K, g))
-    ws = dense_ws(T, N, K)
-    r = torch.randn(T, N, generator=g).cuda()
-    y = torch.empty(T, N, device="cuda")
-    B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, y, ws))
-    B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, r, ws))
-    assert torch.equal(r, y)
+    for T, N, K in [(33, 257, 512), (5, 257, 512), (300, 5001, 640), (300, 5000, 640), (100, 257, 640)]:
+        xq, xs = (t.cuda() for t in R.activations(T, K, g))
+        wq, s = (t.cuda() for t in R.weights(N, K, g))
+        ws = dense_ws(T, N, K)
+        r = torch.randn(T, N, generator=g).cuda()
+        y = torch.empty(T, N, device="cuda")
+        B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, y, ws))
+        B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, r, ws))
+        assert torch.equal(r, y)
 
 
 def test_matmul_non_finite_stays_in_its_row_and_column(colimoe):
