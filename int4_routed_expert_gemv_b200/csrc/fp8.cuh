@@ -26,9 +26,10 @@ __host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / 
 // that is not far below the smallest code is safe.  Scales outside 2^-90 .. 2^90 come into that
 // range, with v, by a power of two.  (A branch to a division per pair of codes took 2.4 us a tile of
 // 128 rows by 128 columns, as long as the SwiGLU.)
-struct Quantizer {
+struct alignas(16) Quantizer {
     float scale, r, by, s;      // s: scale * by, 0 for an infinite scale (finite values get code 0)
 
+    Quantizer() = default;
     // max_bits: bits of the largest |v| (a NaN's are above every number's)
     __device__ __forceinline__ explicit Quantizer(uint32_t max_bits)
     {

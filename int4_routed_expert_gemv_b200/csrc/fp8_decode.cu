@@ -64,6 +64,7 @@ struct Smem {
     float scale[kSlots][2][NT];
     uint32_t mask[kSlots];              // DOWN: columns of the step's expert
     uint32_t top[2][4][C];              // maxima of the SwiGLU rows, by warp
+    Quantizer quantizer[2][C];          // of each column
     int col_pos[NT];
     uint32_t tmem;
     int n_groups, last;
@@ -439,18 +440,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                     if (lane == 0) sm.top[wg][q][j] = t;
                 }
                 named_bar(2 + wg, 128);
-                const int ib = fp8_blocks(p.I);
+                // a column's quantiser, with its divisions, is made by one lane
+                int pos[C];
+#pragma unroll
+                for (int j = 0; j < C; j++) pos[j] = sm.col_pos[wg * C + j];
+                if (q == 0 && lane < mine && sm.col_pos[wg * C + lane] >= 0) {
+                    const Quantizer qz(
+                        max(max(sm.top[wg][0][lane], sm.top[wg][1][lane]), max(sm.top[wg][2][lane], sm.top[wg][3][lane])));
+                    sm.quantizer[wg][lane] = qz;
+                    p.hs[(size_t)sm.col_pos[wg * C + lane] * fp8_blocks(p.I) + rb] = qz.scale;
+                }
+                named_bar(2 + wg, 128);
 #pragma unroll
                 for (int j = 0; j < C; j++) {
                     if (j >= mine) break;
-                    const int pos = sm.col_pos[wg * C + j];
-                    if (pos < 0 || i >= p.I) continue;
-                    const Quantizer qz(
-                        max(max(sm.top[wg][0][j], sm.top[wg][1][j]), max(sm.top[wg][2][j], sm.top[wg][3][j])));
-                    p.hq[(size_t)pos * p.I + i] = (uint8_t)qz.codes(acc[0][j], 0.0f);
-                    if (row == 0) p.hs[(size_t)pos * ib + rb] = qz.scale;
+                    if (pos[j] < 0 || i >= p.I) continue;
+                    const Quantizer qz = sm.quantizer[wg][j];
+                    p.hq[(size_t)pos[j] * p.I + i] = (uint8_t)qz.codes(acc[0][j], 0.0f);
                 }
-                named_bar(2 + wg, 128);      // the maxima are read before the next tile's
             }
         }
     } else if (MODE != FP8_DENSE && blockIdx.x == 0) {

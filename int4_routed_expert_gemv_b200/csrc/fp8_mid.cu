@@ -5,8 +5,8 @@
 // tile, and the tokens, 64 columns, on its N side: a K step of 128 brings a CTA 32 KB of weights
 // and takes it less time than those take to arrive.  The pairs of fp8_pair.cu bring a CTA 16 KB a
 // step, and their step, 1000 cycles, is what 64 experts of 8 rows each waited for (GLM-shaped
-// gate/up of 64 tokens: 427 us, against 250 for reading the weights).  Here, bounded by those
-// reads: gate/up of 17 tokens 241 us (6.0 TB/s) and of 64 tokens 311 us, dense 12288 x 6144 for
+// gate/up of 64 tokens: 392 us, against 250 for reading the weights).  Here, bounded by those
+// reads: gate/up of 17 tokens 230 us (6.1 TB/s) and of 64 tokens 266 us (6.2 TB/s), dense 12288 x 6144 for
 // 64 tokens 24 us (3.1 TB/s: 48 tiles of 48 K steps, joined once each).
 //
 // The columns of a tile are rows of one group, one after another: tokens (DENSE), or an expert's
@@ -48,6 +48,7 @@ struct Smem {
     uint8_t stage[kStages][kStage];
     float scale[kSlots][2][NT];
     uint32_t top[2][4][C];              // maxima of the SwiGLU rows, by warp
+    Quantizer quantizer[2][C];          // of each column
     Groups<kGroups> groups;
     int first[kGroups];
     uint32_t tmem;
@@ -369,17 +370,23 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mid_kernel(const __grid_const
                     if (lane == 0) sm.top[wg][q][j] = t;
                 }
                 named_bar(2 + wg, 128);
+                // a column's quantiser is made by one lane: with its divisions in every thread, GLM-shaped gate/up of 64
+                // tokens took 290 us, so 266
                 const int ib = fp8_blocks(p.I);
+                if (q == 0 && lane < mine) {
+                    const Quantizer qz(
+                        max(max(sm.top[wg][0][lane], sm.top[wg][1][lane]), max(sm.top[wg][2][lane], sm.top[wg][3][lane])));
+                    sm.quantizer[wg][lane] = qz;
+                    p.hs[(size_t)(tl.g.base + col0 + lane) * ib + tl.rb] = qz.scale;
+                }
+                named_bar(2 + wg, 128);
+                uint8_t* to = p.hq + (size_t)(tl.g.base + col0) * p.I + i;
 #pragma unroll
                 for (int j = 0; j < C; j++) {
                     if (j >= mine) break;
-                    const size_t pos = (size_t)(tl.g.base + col0 + j);
-                    const Quantizer qz(
-                        max(max(sm.top[wg][0][j], sm.top[wg][1][j]), max(sm.top[wg][2][j], sm.top[wg][3][j])));
-                    if (i < p.I) p.hq[pos * p.I + i] = (uint8_t)qz.codes(acc[0][j], 0.0f);
-                    if (row == 0) p.hs[pos * ib + tl.rb] = qz.scale;
+                    const Quantizer qz = sm.quantizer[wg][j];
+                    if (i < p.I) to[(size_t)j * p.I] = (uint8_t)qz.codes(acc[0][j], 0.0f);
                 }
-                named_bar(2 + wg, 128);      // the maxima are read before the next tile's
             }
         }
     }

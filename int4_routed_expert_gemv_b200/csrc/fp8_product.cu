@@ -184,16 +184,24 @@ inline size_t partial_bytes(int64_t T)
 }
 
 // Batches above 16 tokens for which reading the weights counts more than the tensor rate: up to
-// so many tokens in all (DENSE), or rows of an expert on the average.  Both sides measured, us, with
-// fp8_mid.cu / fp8_pair.cu: dense 12288 x 6144, 64 tokens 24 / 34, 128 tokens 42 / 36; GLM-shaped
-// experts chosen evenly, gate/up of 32 rows 339 / 451, 48 rows 367 / 460, 64 rows 481 / 465 (unevenly, 50
-// rows 256 / 241, and at hidden 1024 32 rows 51 / 44); down of 64 rows 232 / 294, 96 rows 308 / 316, 128
-// rows 399 / 360.
-constexpr int kMidTokens = 64, kMidGateUp = 32, kMidDown = 80;
+// so many tokens in all (DENSE), or rows of an expert on the average; for gate/up fewer where there are
+// few K steps to a tile, since its 64 tokens' SwiGLU and codes then take longer than the weights.  fp8_mid.cu /
+// fp8_pair.cu, us: dense 12288 x 6144, 64 tokens 24 / 34, 128 tokens 41 / 35; gate/up at hidden 6144 and
+// intermediate 2048 over even lists, 32 rows 296 / 416, 48 rows 313 / 430, 96 rows 566 / 455; over uneven
+// ones at 4096 and 1024, 16 rows 86 / 107, 32 rows 133 / 130, 48 rows 157 / 148; at 2048 and 768, 32 rows 92 / 105, 48
+// rows 121 / 117; at 1024 and 512, 16 rows 26 / 31, 32 rows 35 / 34; at 512 and 256, 4 rows 13.7 / 12.3, 32 rows 15.4 / 13.3;
+// down over even lists at 6144, 64 rows 229 / 291, 96 rows 307 / 316, 128 rows 391 / 356.
+constexpr int kMidTokens = 64, kMidGateUp = 48, kMidDown = 80;
 
-bool mid_batch(int mode, int64_t T, int k, int E)
+bool mid_batch(int mode, int64_t T, int k, int E, int K)
 {
-    return mode == FP8_DENSE ? T <= kMidTokens : T * k <= (int64_t)(mode == FP8_DOWN ? kMidDown : kMidGateUp) * E;
+    if (mode == FP8_DENSE) return T <= kMidTokens;
+    int rows = kMidDown;
+    if (mode == FP8_GATE_UP) {
+        rows = 6 * (fp8_blocks(K) - 4);
+        if (rows > kMidGateUp) rows = kMidGateUp;
+    }
+    return T * k <= (int64_t)rows * E;
 }
 
 // Output rows that do not begin on 16 bytes leave the pairs slowly, which few K steps do not hide.  fp8_mid.cu /
@@ -217,7 +225,7 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     memset(&p, 0, sizeof(p));
     const bool decode = a.T <= kDecodeTokens;
     const bool ragged = a.mode == FP8_DENSE && a.N % (a.y_bf16 ? 8 : 4) != 0;
-    const bool mid = !decode && (mid_batch(a.mode, a.T, a.k, a.E) || (ragged && a.K <= kMidCols));
+    const bool mid = !decode && (mid_batch(a.mode, a.T, a.k, a.E, a.H) || (ragged && a.K <= kMidCols));
     // rows of a token box (1: rows gathered one by one)
     const int box = mid ? 16 : !decode ? 128 : a.mode == FP8_DOWN ? 1 : 16;
     uint8_t* gathered = a.scratch + partial_bytes(a.T);

@@ -251,27 +251,28 @@ def test_norm_codes_at_every_scale(colimoe):
 # ------------------------------------------------------------------------------------------------
 # experts
 # ------------------------------------------------------------------------------------------------
-@pytest.mark.parametrize("T", [16, 60, 400])
-def test_swiglu_over_its_range(colimoe, T):
+@pytest.mark.parametrize("T,H", [(16, 128), (60, 1024), (60, 128), (400, 128)])
+def test_swiglu_over_its_range(colimoe, T, H):
     # one column of h: g = u = +-xs, so its scale is silu(g) * g / 448 with all of fp32
-    H, I = 128, 64
+    I, E = 64, 4
     v = torch.cat([torch.linspace(-79, 200, T - 8), torch.tensor([0.0, 1e-30, -1e-30, 1e-3, -1e-3, 1e4, -1e4, -95.0])])
     x = torch.zeros(T, H, dtype=torch.uint8)
     x[:, 0] = torch.where(v < 0, 0xB8, 0x38).to(torch.uint8)               # e4m3 -1 and 1
     one = torch.zeros(I, H, dtype=torch.uint8)
     one[0, 0] = 0x38
     blob = torch.cat([one.reshape(-1), one.reshape(-1), torch.zeros(H * I, dtype=torch.uint8),
-                      torch.ones(3).view(torch.uint8)])
+                      torch.ones(3 * R.blocks(H)).view(torch.uint8)])
     stride = (blob.numel() + 255) // 256 * 256
-    experts = torch.zeros(2, stride, dtype=torch.uint8)
+    experts = torch.zeros(E, stride, dtype=torch.uint8)
     experts[0, :blob.numel()] = blob
     experts = experts.cuda()
-    dims, weights = B.make_dims(H, I, 2, 1, 0), B.make_weights(None, None, experts, None, stride)
-    lst = [t.cuda() for t in R.lists(torch.zeros(T, 1, dtype=torch.int32), 2)]
+    dims, weights = B.make_dims(H, I, E, 1, 0), B.make_weights(None, None, experts, None, stride)
+    lst = [t.cuda() for t in R.lists(torch.zeros(T, 1, dtype=torch.int32), E)]
     ws = torch.zeros(B.coli_moe_workspace_bytes_fp8(dims, T), dtype=torch.uint8, device="cuda")
     B.check(B.coli_moe_workspace_init(ws))
     hq, hs = torch.empty(T, I, dtype=torch.uint8, device="cuda"), torch.empty(T, 1, device="cuda")
-    B.check(B.coli_moe_gate_up_fp8(dims, weights, x.cuda(), v.abs()[:, None].cuda(), T, *lst, hq, hs, ws))
+    xs = v.abs()[:, None].repeat(1, R.blocks(H)).cuda()
+    B.check(B.coli_moe_gate_up_fp8(dims, weights, x.cuda(), xs, T, *lst, hq, hs, ws))
     assert B.coli_moe_read_status(ws) == (B.COLI_OK, 0)
     g = v.double()
     h = g * torch.sigmoid(g) * g
@@ -382,6 +383,16 @@ def test_gate_up(colimoe, H, I, E, k, ns, T):
 @pytest.mark.parametrize("T", [1, 4, 16, 17, 70, 200])
 def test_down(colimoe, H, I, E, k, ns, T):
     Case(H, I, E, k, ns, T, seed=T, hot=T % 2 == 0).check_down(residual=T % 3 != 0)
+
+
+@pytest.mark.parametrize("T", [17, 70, 150])
+@pytest.mark.parametrize("hot", [False, True])
+@pytest.mark.parametrize("I", [64, 320])
+def test_batches_in_between(colimoe, T, hot, I):
+    # few rows an expert on the average, and one expert with all tokens; odd sizes of K and of the last row block
+    c = Case(1088, I, 16, 2, 1, T, seed=T, hot=hot)
+    c.check_gate_up()
+    c.check_down()
 
 
 @pytest.mark.parametrize("T", [100, 330])
