@@ -329,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
             for (int m = 0; m < 2; m++)
 #pragma unroll
                 for (int j = 0; j < C; j++) acc[m][j] = 0.0f;
+            __syncwarp();        // tensor memory loads are a whole warp's
             for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                 const int b = n % kBufs, s = n % kSlots;
                 if (!dead && !mbar_wait(&sm.sc_full[s], (n / kSlots) & 1, p.status, kSite + 8)) dead = true;

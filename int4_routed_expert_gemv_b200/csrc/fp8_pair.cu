@@ -291,69 +291,7 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap* map, int c0, int 
     }
 }
 
-// A warp's part of the residual on its way into L2: a lane a row, two runs of 64 columns.
-template <class Y>
-__device__ __forceinline__ void prefetch_rows(const Y* residual, int rows, int c0, int y0, int left, int lane)
-{
-    if (lane >= left) return;
-#pragma unroll
-    for (int run = 0; run < 2; run++) {
-        const int last = min(64, rows - c0 - run * kM) - 1;
-        if (last < 0) break;
-        const Y* at = residual + (size_t)(y0 + lane) * rows + c0 + run * kM;
-#pragma unroll
-        for (int j = 0; j <= 64; j += 32)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + min(j, last)));
-    }
-}
-
-// The same without boxes, for rows that do not begin on 16 bytes (the first `left` rows from y0):
-// 32 columns at a time go through shared memory, so that a warp writes 32 consecutive values of a
-// row.  The residual is in L2 by then: read from HBM here, it took 4000 x 4002 x 2048 in
-// fp32 from 70 us without one to 164; so it takes 95.  (Pieces of 16 bytes that begin where memory does,
-// 256 columns a row, took 79 without one and 113 with it.)
-template <class Y>
-__device__ __forceinline__ void store_rows(Y* y, const Y* residual, int rows, int c0, int y0, int left, const float (&acc)[C],
-                                           float* stage, int lane)
-{
-    constexpr int P = 33, B = 16;      // rows whose loads are under way together
-    if (lane == 0) boxes_read();
-#pragma unroll
-    for (int j0 = 0; j0 < C; j0 += 32) {
-        const int col = c0 + (j0 >> 6) * kM + (j0 & 63) + lane;
-        const int n = col < rows ? left : 0;
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 32; j++) stage[lane * P + j] = acc[j0 + j];
-        __syncwarp();
-#pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += B) {
-            const size_t at = (size_t)(y0 + r0) * rows + col;
-            // (nothing but the loads and the stores under a condition: a branch around more of it would
-            // make the rows wait for one another)
-            Y v[B];
-            float f[B];
-#pragma unroll
-            for (int r = 0; r < B; r++)
-                if (residual && r0 + r < n) v[r] = residual[at + (size_t)r * rows];
-#pragma unroll
-            for (int r = 0; r < B; r++) f[r] = stage[(r0 + r) * P + lane];
-            if (residual) {
-#pragma unroll
-                for (int r = 0; r < B; r++) f[r] += (float)v[r];
-            }
-#pragma unroll
-            for (int r = 0; r < B; r++)
-                if (r0 + r < n) y[at + (size_t)r * rows] = (Y)f[r];
-        }
-    }
-    __syncwarp();
-    fence_async_smem();      // later copies into the same memory
-}
-
-// ROWS (DENSE): outputs by store_rows.  A kernel of its own: beside the boxes it took those from 115 to
-// 120 us at 4096 x 4096 x 6144, by registers.
-template <int MODE, bool ROWS = false>
+template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ Params p)
 {
@@ -481,6 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 commit_pair(&sm.mma_done[odd]);
                 mbar_wait(&sm.mma_done[odd], 0, p.status, kSite + 5);
             }
+            // the commits' arrivals in the other CTA have all come before it ends
+            if (lane == 0 && rank == 1) mbar_wait(&sm.mma_done[warp == 11], 0, p.status, kSite + 6);
         } else if (warp == 10) {
             // ------------------------------- briefs -----------------------------------------
             uint32_t m = 0;
@@ -593,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // the residual of a whole tile is asked for a few steps into it, when the stores of
             // the tile before have read the boxes
             const int c0 = 2 * w.rb * kM + wg * 64;       // output columns: two runs of 64
-            bool ask = MODE == FP8_DENSE && !ROWS && p.residual && p.slices == 1 && left > 0;
+            bool ask = MODE == FP8_DENSE && p.residual && p.slices == 1 && left > 0;
             auto ask_now = [&]() {
                 if (lane == 0) {
                     if (p.y_bf16) ask_residual<__nv_bfloat16>(p, c0, w.y0, sm.box[warp][0], &sm.res[warp]);
@@ -604,10 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 asked++;
             };
             const bool whole = it.kb1 - it.kb0 == p.kb;
-            if (ROWS && p.residual) {
-                if (p.y_bf16) prefetch_rows(reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.y0, left, lane);
-                else prefetch_rows(reinterpret_cast<const float*>(p.residual), p.rows, c0, w.y0, left, lane);
-            }
+            __syncwarp();        // tensor memory loads are a whole warp's
             if (left > 0) {
                 // scales of four K steps at a time, fetched four steps ahead
                 for (int kb = it.kb0 & ~3; kb < it.kb1; kb += 4) {
@@ -693,15 +630,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // (H is a multiple of 64: a box has all of its columns)
                     store_boxes<float, false, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane,
                                                   left < 32 ? p.z : nullptr, left);
-                } else if constexpr (ROWS) {
-                    float* plain = reinterpret_cast<float*>(sm.box[warp][0]);
-                    if (p.y_bf16)
-                        store_rows<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(p.y),
-                                                  reinterpret_cast<const __nv_bfloat16*>(p.residual), p.rows, c0, w.y0, left, acc,
-                                                  plain, lane);
-                    else
-                        store_rows<float>(reinterpret_cast<float*>(p.y), reinterpret_cast<const float*>(p.residual), p.rows, c0,
-                                          w.y0, left, acc, plain, lane);
                 } else if (p.slices > 1) {
                     store_boxes<float, false, NB>(&p.out, c0, w.y0, it.slice, p.pitch, acc, sm.box[warp][0], lane);
                 } else if (p.residual) {
@@ -757,12 +685,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int MODE, bool ROWS = false>
+template <int MODE>
 cudaError_t launch(const Params& p, int grid, cudaStream_t s)
 {
-    const cudaError_t e = allow_smem<fp8_pair_kernel<MODE, ROWS>>(kSmem<MODE>);
+    const cudaError_t e = allow_smem<fp8_pair_kernel<MODE>>(kSmem<MODE>);
     if (e != cudaSuccess) return e;
-    return launch_early<fp8_pair_kernel<MODE, ROWS>>(grid, kThreads, kSmem<MODE>, s, p);
+    return launch_early<fp8_pair_kernel<MODE>>(grid, kThreads, kSmem<MODE>, s, p);
 }
 
 }  // namespace
@@ -770,10 +698,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t s)
 cudaError_t fp8_pair_launch(int mode, const fp8::Params& p, int num_sms, cudaStream_t s)
 {
     const int grid = (num_sms < kFp8Ctas ? num_sms : kFp8Ctas) / 2 * 2;
-    return mode == FP8_GATE_UP ? launch<FP8_GATE_UP>(p, grid, s)
-           : mode == FP8_DOWN  ? launch<FP8_DOWN>(p, grid, s)
-           : p.boxed           ? launch<FP8_DENSE>(p, grid, s)
-                               : launch<FP8_DENSE, true>(p, grid, s);
+    return mode == FP8_DENSE     ? launch<FP8_DENSE>(p, grid, s)
+           : mode == FP8_GATE_UP ? launch<FP8_GATE_UP>(p, grid, s)
+                                 : launch<FP8_DOWN>(p, grid, s);
 }
 
 }  // namespace coli

@@ -204,11 +204,6 @@ bool mid_batch(int mode, int64_t T, int k, int E, int K)
     return T * k <= (int64_t)rows * E;
 }
 
-// Output rows that do not begin on 16 bytes leave the pairs slowly, which few K steps do not hide.  fp8_mid.cu /
-// fp8_pair.cu, us: 543 x 7298 x 208 to bf16 14 / 22, onto a residual 20 / 31; 187 x 2259 x 320 8.7 / 12.3; 725 x 3846
-// x 272 onto a residual 21.0 / 19.8; 4000 x 4001 x 512 onto a residual 68 / 67, x 1024 63 / 52.
-constexpr int kMidCols = 3 * kFp8Block;
-
 }  // namespace
 
 size_t fp8_scratch_bytes(int mode, int64_t T, int H, int k, int n_shared)
@@ -224,8 +219,10 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
     Params p;
     memset(&p, 0, sizeof(p));
     const bool decode = a.T <= kDecodeTokens;
+    // Rows of y that do not begin on 16 bytes go to the kernel that writes single values: the pairs write by
+    // tensor copies (4000 x 4001 x 2048 onto an fp32 residual 120 us, x 4000 with the pairs 62).
     const bool ragged = a.mode == FP8_DENSE && a.N % (a.y_bf16 ? 8 : 4) != 0;
-    const bool mid = !decode && (mid_batch(a.mode, a.T, a.k, a.E, a.H) || (ragged && a.K <= kMidCols));
+    const bool mid = !decode && (ragged || mid_batch(a.mode, a.T, a.k, a.E, a.H));
     // rows of a token box (1: rows gathered one by one)
     const int box = mid ? 16 : !decode ? 128 : a.mode == FP8_DOWN ? 1 : 16;
     uint8_t* gathered = a.scratch + partial_bytes(a.T);
@@ -290,12 +287,12 @@ cudaError_t fp8_product_launch(const Fp8ProductArgs& a, cudaStream_t s)
             p.slices = most < 2 ? 1 : most < fit ? most : fit;
         }
         p.pitch = (a.N + 3) / 4 * 4;
-        const int es = a.y_bf16 && p.slices == 1 ? 2 : 4;
-        p.boxed = p.slices > 1 || a.N % (16 / es) == 0;
-        if (mid) p.boxed = 0;
-        else if (p.slices > 1) ok &= out_map(&p.out, p.partial, 4, p.pitch, a.T, p.slices);
-        else if (p.boxed) ok &= out_map(&p.out, a.y, es, a.N, a.T, 1);
-        if (p.boxed && p.slices == 1 && a.residual) ok &= out_map(&p.res, a.residual, es, a.N, a.T, 1);
+        const int es = a.y_bf16 ? 2 : 4;
+        if (!mid && p.slices > 1) ok &= out_map(&p.out, p.partial, 4, p.pitch, a.T, p.slices);
+        if (!mid && p.slices == 1) {
+            ok &= out_map(&p.out, a.y, es, a.N, a.T, 1);
+            if (a.residual) ok &= out_map(&p.res, a.residual, es, a.N, a.T, 1);
+        }
         if (!ok) return cudaErrorInvalidValue;
     }
     auto product = [&]() {

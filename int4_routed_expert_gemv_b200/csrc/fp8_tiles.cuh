@@ -40,7 +40,6 @@ struct Params {
     float* hs;
     float* z;                     // DOWN above 16 tokens: [T*k + T*n_shared][rows], in list order
     int32_t* z_row;               // [T*k] 1 + row of z of t * k + slot, 0 where the lists leave it out
-    int boxed;                    // rows of the output begin on 16 bytes: out and res are set
     float* partial;               // sums of the parts of split tiles, or slices [slices][T][pitch]
     int slices, pitch;
     uint32_t* tickets;            // parts that have arrived, by the first part's worker

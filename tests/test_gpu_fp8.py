@@ -67,6 +67,22 @@ def test_matmul_rows_of_any_length(colimoe, dtype, T, N, K, residual):
     run_matmul(T, N, K, dtype, residual)
 
 
+@pytest.mark.parametrize("T,N,K,residual", [(1382, 3081, 1776, True), (1382, 3081, 1776, False), (1382, 3080, 1776, True),
+                                            (70, 12291, 640, True)])
+def test_matmul_calls_in_a_row(colimoe, T, N, K, residual):
+    # a warp with 6 rows of a tile, every tile split, one call behind the other
+    g = torch.Generator().manual_seed(5)
+    xq, xs = (t.cuda() for t in R.activations(T, K, g))
+    wq, s = (t.cuda() for t in R.weights(N, K, g))
+    r = torch.randn(T, N, generator=g).cuda() if residual else None
+    ws = dense_ws(T, N, K)
+    ys = [torch.empty(T, N, device="cuda") for _ in range(3)]
+    for i in range(60):
+        B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, ys[i % 3], ws))
+    assert B.coli_moe_read_status(ws) == (B.COLI_OK, 0)
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
 def test_matmul_many_tiles(colimoe):
     # more tiles than CTAs, so whole tiles and split ones in one launch
     for T, N, K in [(1024, 6144, 256), (2049, 4100, 128)]:
