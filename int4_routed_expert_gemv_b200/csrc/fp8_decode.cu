@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                 }
                 for (int kb = sg.k0; kb < sg.k1; kb++, n++) {
                     const int s = n % kStages;
-                    if (!dead && !mbar_wait(&sm.empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
+                    warp_wait(dead, &sm.empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1);
                     if (dead) continue;
                     uint8_t* st = sm.stage[s];
                     if (lane == 0) {
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
             while (sch.next(it)) {
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int s = n % kStages, b = n % kBufs;
-                    if (!dead && !mbar_wait(&sm.acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
-                    if (!dead && !mbar_wait(&sm.full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
+                    lane_wait(dead, &sm.acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3);
+                    lane_wait(dead, &sm.full[s], (n / kStages) & 1, p.status, kSite + 4);
                     tc_fence_after();
                     if (!dead) {
                         const uint8_t* st = sm.stage[s];
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                     for (int i = 0; i < B; i++) {
                         if (kb + i >= sg.k1) break;
                         const int slot = n % kSlots;
-                        if (!dead && !mbar_wait(&sm.sc_empty[slot], ((n / kSlots) & 1) ^ 1, p.status, kSite + 6)) dead = true;
+                        warp_wait(dead, &sm.sc_empty[slot], ((n / kSlots) & 1) ^ 1, p.status, kSite + 6);
                         sm.scale[slot][m][j] = s[i];
                         if (MODE == FP8_DOWN && lane == 0) sm.mask[slot] = mask;
                         __syncwarp();
@@ -329,11 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
             for (int m = 0; m < 2; m++)
 #pragma unroll
                 for (int j = 0; j < C; j++) acc[m][j] = 0.0f;
-            __syncwarp();        // tensor memory loads are a whole warp's
             for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                 const int b = n % kBufs, s = n % kSlots;
-                if (!dead && !mbar_wait(&sm.sc_full[s], (n / kSlots) & 1, p.status, kSite + 8)) dead = true;
-                if (!dead && !mbar_wait(&sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                warp_wait(dead, &sm.sc_full[s], (n / kSlots) & 1, p.status, kSite + 8);
+                warp_wait(dead, &sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7);
                 tc_fence_after();
                 if (mine > 0) {
                     uint32_t v[2][C];

@@ -369,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int row0 = base + tl.t0 + rank * kM;
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int s = n % kStages;
-                    if (!dead && !mbar_wait(&sm.empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1)) dead = true;
+                    warp_wait(dead, &sm.empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1);
                     if (dead) continue;
                     if (lane == 0) {
                         uint8_t* st = sm.stage[s];
@@ -404,8 +404,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int s = n % kStages, b = n % kBufs;
                         const uint8_t* st = sm.stage[s];
                         const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + kTile);
-                        if (!dead && !mbar_wait(&sm.full[s], (n / kStages) & 1, p.status, kSite + 4)) dead = true;
-                        if (!dead && !mbar_wait(&sm.acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3)) dead = true;
+                        lane_wait(dead, &sm.full[s], (n / kStages) & 1, p.status, kSite + 4);
+                        lane_wait(dead, &sm.acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3);
                         tc_fence_after();
                         if (!dead) {
 #pragma unroll
@@ -429,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 more = sch.next(it);
                 Tile tl{};
                 if (more) tl = tile_of(p, sm.groups, sm.first, n_groups, NT, it.tile);
-                if (!dead && !mbar_wait(&sm.brief_empty[slot], ((m / kBriefs) & 1) ^ 1, p.status, kSite + 11)) dead = true;
+                warp_wait(dead, &sm.brief_empty[slot], ((m / kBriefs) & 1) ^ 1, p.status, kSite + 11);
                 if (lane == 0) {
                     if (!more) it.tile = -1;
                     sm.brief[slot] = Brief{it, tl.rb, tl.g.expert, tl.t0, tl.n, tl.g.base};
@@ -492,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         auto look_up = [&](Work& w) {
             const int slot = briefs % kBriefs;
-            if (!dead && !mbar_wait(&sm.brief_full[slot], (briefs / kBriefs) & 1, p.status, kSite + 12)) dead = true;
+            warp_wait(dead, &sm.brief_full[slot], (briefs / kBriefs) & 1, p.status, kSite + 12);
             const Brief tl = sm.brief[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.brief_empty[slot]);
@@ -544,7 +544,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 asked++;
             };
             const bool whole = it.kb1 - it.kb0 == p.kb;
-            __syncwarp();        // tensor memory loads are a whole warp's
             if (left > 0) {
                 // scales of four K steps at a time, fetched four steps ahead
                 for (int kb = it.kb0 & ~3; kb < it.kb1; kb += 4) {
@@ -561,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; i++) {
                         if (kb + i < it.kb0 || kb + i >= it.kb1) continue;
                         const int b = n % kBufs;
-                        if (!dead && !mbar_wait(&sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                        warp_wait(dead, &sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7);
                         tc_fence_after();
                         const uint32_t ta = lane_addr + (uint32_t)(b * 256 + wg * 64);
                         // loads run one chunk of 16 columns ahead of the arithmetic
@@ -585,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // no token in this warp: only hand the buffers on
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
                     const int b = n % kBufs;
-                    if (!dead && !mbar_wait(&sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7)) dead = true;
+                    warp_wait(dead, &sm.acc_full[b], (n / kBufs) & 1, p.status, kSite + 7);
                     __syncwarp();
                     if (lane == 0) arrive_pair(ae + b * 8);
                 }
@@ -634,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     store_boxes<float, false, NB>(&p.out, c0, w.y0, it.slice, p.pitch, acc, sm.box[warp][0], lane);
                 } else if (p.residual) {
                     if (ask) ask_now();
-                    if (!dead && !mbar_wait(&sm.res[warp], (asked - 1) & 1, p.status, kSite + 9)) dead = true;
+                    warp_wait(dead, &sm.res[warp], (asked - 1) & 1, p.status, kSite + 9);
                     if (p.y_bf16) store_boxes<__nv_bfloat16, true, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane);
                     else store_boxes<float, true, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane);
                 } else {

@@ -1,0 +1,31 @@
+"""How the fp8 kernels wait, read from their sources: a wait that gives up, or lanes that leave a wait at
+different times, cannot be provoked on a GPU in a test."""
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+KERNELS = ["fp8_decode.cu", "fp8_mid.cu", "fp8_pair.cu"]
+
+
+def source(name: str) -> str:
+    with open(os.path.join(ROOT, "int4_routed_expert_gemv_b200", "csrc", name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_tensor_memory_loads_follow_a_whole_warps_wait(name):
+    # every lane polls for itself: only the vote in warp_wait brings the warp together before tcgen05.ld.sync.aligned
+    calls = re.findall(r"\b(mbar_wait|lane_wait|warp_wait|tmem_ld\d+)\(", source(name))
+    loads = [i for i, c in enumerate(calls) if c.startswith("tmem_ld")]
+    assert loads
+    for i in loads:
+        waits = [c for c in calls[:i] if not c.startswith("tmem_ld")]
+        assert waits[-1] == "warp_wait"
+    assert "!mbar_wait" not in source(name), "one lane's answer would be its own"
+
+
+def test_the_vote_is_the_whole_warps():
+    body = re.search(r"void warp_wait\([^)]*\)\s*\{(.*?)\n\}", source("fp8_tiles.cuh"), re.S).group(1)
+    assert re.search(r"dead = !__all_sync\(0xffffffffu, ok\);\s*$", body)
