@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 
     if (warp == 8) {
         // ------------------------------- TMA producer -----------------------------------
-        uint32_t n = 0;
+        uint32_t n = 0, sent = 0;
         while (sch.next(it)) {
             Segments<MODE> segs(p, it);
             while (segs.next(sg)) {
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                     const int s = n % kStages;
                     warp_wait(dead, &sm.empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1);
                     if (dead) continue;
+                    sent = n + 1;
                     uint8_t* st = sm.stage[s];
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&sm.full[s], kStage);
@@ -231,13 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
             }
         }
         // no copy is in flight when the CTA ends
-        if (lane == 0) {
-            const uint32_t last = n < (uint32_t)kStages ? n : (uint32_t)kStages;
-            for (uint32_t i = 0; i < last; i++) {
-                const uint32_t m = n - 1 - i;
-                mbar_wait(&sm.full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
-            }
-        }
+        if (lane == 0) drain(sm.full, kStages, sent, p.status, kSite + 2);
     } else if (warp == 9) {
         // ------------------------------- MMA issuer -------------------------------------
         if (lane == 0) {

@@ -353,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 8) {
             // ----------------------------- TMA producer ---------------------------------
-            uint32_t n = 0;
+            uint32_t n = 0, sent = 0;
             while (sch.next(it)) {
                 const Tile tl = tile_of(p, sm.groups, sm.first, n_groups, NT, it.tile);
                 const int shared = tl.g.expert < 0 ? 1 : 0;
@@ -371,6 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int s = n % kStages;
                     warp_wait(dead, &sm.empty[s], ((n / kStages) & 1) ^ 1, p.status, kSite + 1);
                     if (dead) continue;
+                    sent = n + 1;
                     if (lane == 0) {
                         uint8_t* st = sm.stage[s];
                         const uint32_t bar = map_to(&sm.full[s], 0);
@@ -383,13 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             // no copy of the pair is in flight when it ends
-            if (lane == 0 && rank == 0) {
-                const uint32_t last = n < (uint32_t)kStages ? n : (uint32_t)kStages;
-                for (uint32_t i = 0; i < last; i++) {
-                    const uint32_t m = n - 1 - i;
-                    mbar_wait(&sm.full[m % kStages], (m / kStages) & 1, p.status, kSite + 2);
-                }
-            }
+            if (lane == 0 && rank == 0) drain(sm.full, kStages, sent, p.status, kSite + 2);
         } else if (warp == 9 || warp == 11) {
             // ----------------------------- MMA issuers -----------------------------------
             // K steps alternate between the two: an issuer is held up until its MMAs have nearly
@@ -430,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 Tile tl{};
                 if (more) tl = tile_of(p, sm.groups, sm.first, n_groups, NT, it.tile);
                 warp_wait(dead, &sm.brief_empty[slot], ((m / kBriefs) & 1) ^ 1, p.status, kSite + 11);
-                if (lane == 0) {
+                if (lane == 0 && !dead) {      // (a slot that was not handed back may still be read)
                     if (!more) it.tile = -1;
                     sm.brief[slot] = Brief{it, tl.rb, tl.g.expert, tl.t0, tl.n, tl.g.base};
                     mbar_arrive(&sm.brief_full[slot]);
@@ -497,7 +492,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.brief_empty[slot]);
             briefs++;
-            if (dead || tl.it.tile < 0) return false;
+            if (dead) {
+                // no brief any more: the same items, without tokens, since the other warps wait for this one
+                // at named barriers
+                w.left = w.rb = w.expert = w.xrow = w.y0 = 0;
+                w.orow = -1;
+                Schedule again;      // (made here: registers are dear)
+                again.init(sm.tiles, p.kb, (int)n_clusters(), (int)cluster_id(), kLeast, kJoin, p.slices);
+                return again.at((int)briefs - 1, w.it);
+            }
+            if (tl.it.tile < 0) return false;
             w.it = tl.it;
             w.rb = tl.rb;
             w.expert = tl.expert;
@@ -632,8 +636,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 } else if (p.slices > 1) {
                     store_boxes<float, false, NB>(&p.out, c0, w.y0, it.slice, p.pitch, acc, sm.box[warp][0], lane);
                 } else if (p.residual) {
-                    if (ask) ask_now();
+                    if (ask && !dead) ask_now();
                     warp_wait(dead, &sm.res[warp], (asked - 1) & 1, p.status, kSite + 9);
+                    if (dead) continue;       // the boxes may still be written to
                     if (p.y_bf16) store_boxes<__nv_bfloat16, true, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane);
                     else store_boxes<float, true, NB>(&p.out, c0, w.y0, 0, p.rows, acc, sm.box[warp][0], lane);
                 } else {
@@ -672,8 +677,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        // this thread's stores are complete
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        // this warp's copies, in and out, are complete
+        if (lane == 0) {
+            if (asked) mbar_wait(&sm.res[warp], (asked - 1) & 1, p.status, kSite + 10);
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();

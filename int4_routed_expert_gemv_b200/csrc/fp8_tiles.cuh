@@ -78,6 +78,12 @@ __device__ __forceinline__ void warp_wait(bool& dead, uint64_t* bar, uint32_t pa
     dead = !__all_sync(0xffffffffu, ok);
 }
 
+// One thread: until the last copies that it sent into a ring of stages have landed.
+__device__ __forceinline__ void drain(uint64_t* full, uint32_t stages, uint32_t sent, uint32_t* status, uint32_t site)
+{
+    for (uint32_t m = sent - min(sent, stages); m < sent; m++) mbar_wait(&full[m % stages], (m / stages) & 1, status, site);
+}
+
 __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -157,7 +163,7 @@ struct Schedule {
 
     // join: what joining the parts of a tile costs, in K steps.  Splitting has to save more;
     // a worker alone streams a quarter faster than all of them together.
-    __device__ void init(int tiles_, int kb_, int G_, int c_, int least, int join, int slices_ = 1)
+    __host__ __device__ void init(int tiles_, int kb_, int G_, int c_, int least, int join, int slices_ = 1)
     {
         slices = slices_;
         tiles = tiles_;
@@ -176,13 +182,13 @@ struct Schedule {
         u1 = start(min(c + 1, n_run));
         t = split + c;
     }
-    __device__ int start(int cc) const { return cc >= n_run ? split * kb : cc * per + min(cc, more); }
-    __device__ int owner(int unit) const
+    __host__ __device__ int start(int cc) const { return cc >= n_run ? split * kb : cc * per + min(cc, more); }
+    __host__ __device__ int owner(int unit) const
     {
         const int big = more * (per + 1);
         return unit < big ? unit / (per + 1) : more + (unit - big) / max(per, 1);
     }
-    __device__ bool next(Item& it)
+    __host__ __device__ bool next(Item& it)
     {
         if (u < u1) {
             it.tile = u / kb;
@@ -193,14 +199,35 @@ struct Schedule {
             return true;
         }
         if (t < tiles * slices) {
-            it.tile = t / slices;
-            it.slice = t - it.tile * slices;
-            it.kb0 = (int)((int64_t)kb * it.slice / slices);
-            it.kb1 = (int)((int64_t)kb * (it.slice + 1) / slices);
+            whole(t, it);
             t += G;
             return true;
         }
         return false;
+    }
+    // Item i, as the (i + 1)-th next() gives it.
+    __host__ __device__ bool at(int i, Item& it) const
+    {
+        const int a = start(min(c, n_run)), b = start(min(c + 1, n_run));
+        const int parts = b > a ? (b - 1) / kb - a / kb + 1 : 0;
+        if (i < parts) {
+            it.tile = a / kb + i;
+            it.kb0 = max(a - it.tile * kb, 0);
+            it.kb1 = min(b - it.tile * kb, kb);
+            it.slice = 0;
+            return true;
+        }
+        const int64_t n = split + c + (int64_t)(i - parts) * G;
+        if (n >= (int64_t)tiles * slices) return false;
+        whole((int)n, it);
+        return true;
+    }
+    __host__ __device__ void whole(int n, Item& it) const
+    {
+        it.tile = n / slices;
+        it.slice = n - it.tile * slices;
+        it.kb0 = (int)((int64_t)kb * it.slice / slices);
+        it.kb1 = (int)((int64_t)kb * (it.slice + 1) / slices);
     }
 };
 

@@ -29,3 +29,21 @@ def test_tensor_memory_loads_follow_a_whole_warps_wait(name):
 def test_the_vote_is_the_whole_warps():
     body = re.search(r"void warp_wait\([^)]*\)\s*\{(.*?)\n\}", source("fp8_tiles.cuh"), re.S).group(1)
     assert re.search(r"dead = !__all_sync\(0xffffffffu, ok\);\s*$", body)
+
+
+def test_a_warp_that_gave_up_goes_through_every_item():
+    # the other warps wait for it at named barriers, which have no limit: no loop over items may end on `dead`
+    for name in KERNELS:
+        assert not re.search(r"dead \|\||\|\| dead|!dead &&[^;]*(next|more)|if \(dead\) (break|return)", source(name)), name
+    look_up = re.search(r"auto look_up = .*?return true;\s*\};", source("fp8_pair.cu"), re.S).group(0)
+    assert re.search(r"if \(dead\) \{[^}]*again\.init\([^}]*return again\.at\(\(int\)briefs - 1, w\.it\);\s*\}", look_up)
+    # and briefs are not overwritten under a warp that still reads them
+    assert "if (lane == 0 && !dead)" in source("fp8_pair.cu")
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_copies_asked_for_are_waited_for(name):
+    # by their own count: after a wait that gave up the step counter runs on
+    s = source(name)
+    assert re.search(r"if \(dead\) continue;\s*sent = n \+ 1;", s)
+    assert re.search(r"drain\(sm\.full, kStages, sent, p\.status", s)
