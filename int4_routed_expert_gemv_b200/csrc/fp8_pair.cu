@@ -414,8 +414,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 commit_pair(&sm.mma_done[odd]);
                 mbar_wait(&sm.mma_done[odd], 0, p.status, kSite + 5);
             }
-            // the commits' arrivals in the other CTA have all come before it ends
-            if (lane == 0 && rank == 1) mbar_wait(&sm.mma_done[warp == 11], 0, p.status, kSite + 6);
         } else if (warp == 10) {
             // ------------------------------- briefs -----------------------------------------
             uint32_t m = 0;
@@ -685,6 +683,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // The commits' arrivals in rank 1 have all come before it ends.  (Its sums are formed by now, so the last MMAs
+    // are done; from the start on this wait would give up in a launch that takes longer than its limit.)
+    if (rank == 1 && tid < 2) mbar_wait(&sm.mma_done[tid], 0, p.status, kSite + 6);
+    __syncwarp();
     cluster_sync();        // the other CTA's barriers and tiles stay in use until here
     if (warp == 9) {
         tc_fence_after();

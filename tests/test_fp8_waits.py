@@ -47,3 +47,11 @@ def test_copies_asked_for_are_waited_for(name):
     s = source(name)
     assert re.search(r"if \(dead\) continue;\s*sent = n \+ 1;", s)
     assert re.search(r"drain\(sm\.full, kStages, sent, p\.status", s)
+
+
+def test_no_wait_of_the_pairs_lasts_a_whole_launch():
+    # rank 1 issues no MMAs: it may wait for the last commits only when its own sums are formed
+    s = source("fp8_pair.cu")
+    at = s.index("if (rank == 1 && tid < 2) mbar_wait(&sm.mma_done[tid]")
+    assert s.index("warp_wait(dead, &sm.acc_full") < s.rindex("__syncthreads();") < at < s.rindex("cluster_sync();")
+    assert len(re.findall(r"wait\([^;]*mma_done", s)) == 2
