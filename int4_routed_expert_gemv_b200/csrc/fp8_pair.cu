@@ -399,8 +399,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int s = n % kStages, b = n % kBufs;
                         const uint8_t* st = sm.stage[s];
                         const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + kTile);
-                        lane_wait(dead, &sm.full[s], (n / kStages) & 1, p.status, kSite + 4);
+                        // In this order: with three stages an issuer sees every other phase of full[s] only, and a
+                        // parity alone cannot tell step n from step n - 6.  The buffer's hand-back says
+                        // that step n - 2 has been added up, hence that step n - 3, the stage's last, had landed.
                         lane_wait(dead, &sm.acc_empty[b], ((n / kBufs) & 1) ^ 1, p.status, kSite + 3);
+                        lane_wait(dead, &sm.full[s], (n / kStages) & 1, p.status, kSite + 4);
                         tc_fence_after();
                         if (!dead) {
 #pragma unroll

@@ -55,3 +55,58 @@ def test_no_wait_of_the_pairs_lasts_a_whole_launch():
     at = s.index("if (rank == 1 && tid < 2) mbar_wait(&sm.mma_done[tid]")
     assert s.index("warp_wait(dead, &sm.acc_full") < s.rindex("__syncthreads();") < at < s.rindex("cluster_sync();")
     assert len(re.findall(r"wait\([^;]*mma_done", s)) == 2
+
+
+def issued_too_early(stages: int, order, steps: int = 13) -> bool:
+    """Every order of events in the pair kernel's ring of `stages` tiles and two accumulator buffers, with two
+    issuers that take the steps in turn: can an MMA be issued before its tiles have landed?  Barriers are what the
+    hardware has, a count of phases of which a wait sees the parity."""
+    # state: steps sent, landed steps (bits), per issuer (its step, waits done), MMAs done (bits), steps added up
+    start = (0, 0, (0, 0), (1, 0), 0, 0)
+    seen, todo = {start}, [start]
+    while todo:
+        sent, landed, a, b, done, added = todo.pop()
+        new = []
+        if sent < steps and (sent < stages or done >> (sent - stages) & 1):
+            new.append((sent + 1, landed, a, b, done, added))
+        for p in range(max(0, sent - stages), sent):
+            if not landed >> p & 1:
+                new.append((sent, landed | 1 << p, a, b, done, added))
+        for i, (n, waits) in enumerate((a, b)):
+            if n >= steps:
+                continue
+            if waits < 2:
+                if order[waits] == "full":
+                    phases = sum(landed >> p & 1 for p in range(n % stages, steps, stages))
+                    ok = phases % 2 != n // stages % 2
+                else:
+                    phases = sum(1 for p in range(n % 2, added, 2))
+                    ok = phases % 2 != (n // 2 % 2) ^ 1
+                to = (n, waits + 1) if ok else None
+            elif not landed >> n & 1:
+                return True
+            else:      # issued; it ends at some later time
+                to = (n + 2, 0)
+            if to:
+                new.append((sent, landed) + ((to, b) if i == 0 else (a, to)) + (done, added))
+        for n in range(steps):
+            if not done >> n & 1 and n < (a, b)[n % 2][0] and (n < 2 or done >> (n - 2) & 1):
+                new.append((sent, landed, a, b, done | 1 << n, added))
+        if added < steps and done >> added & 1:
+            new.append((sent, landed, a, b, done, added + 1))
+        for s in new:
+            if s not in seen:
+                seen.add(s)
+                todo.append(s)
+    assert any(s[5] == steps for s in seen)
+    return False
+
+
+def test_the_pairs_mmas_wait_for_their_tiles():
+    s = source("fp8_pair.cu")
+    order = re.findall(r"lane_wait\(dead, &sm\.(full|acc_empty)\[", s)
+    stages = [int(v) for v in re.search(r"kStages = MODE == FP8_GATE_UP \? (\d+) : (\d+);", s).groups()]
+    assert len(order) == 2 and re.search(r"kBufs = 2;", s)
+    for n in stages:
+        assert not issued_too_early(n, order), (n, order)
+    assert issued_too_early(3, ["full", "acc_empty"]), "the model knows the other order's fault"

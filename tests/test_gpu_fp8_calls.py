@@ -37,3 +37,56 @@ def test_matmul_of_several_seconds(colimoe):
     bound = bound + (ref + bound) * 2.0 ** -8
     got = y[rows][:, cols].cpu().double()
     assert ((got - ref).abs() <= bound).all()
+
+
+def device_inputs(T, N, K, dtype, residual, seed):
+    g = torch.Generator().manual_seed(seed)
+    xq, xs = R.activations(T, K, g)
+    wq, s = R.weights(N, K, g)
+    r = torch.randn(T, N, generator=g).to(dtype) if residual else None
+    return [None if t is None else t.cuda() for t in (xq, xs, wq, s, r)]
+
+
+def check_matmul(y, xq, xs, wq, s, r):
+    """y [T][N] against 64 bits, on the device."""
+    x, w = (q.double() * t.double().repeat_interleave(128, 1)[:, :q.shape[1]]
+            for q, t in ((xq, xs), (wq, s.repeat_interleave(128, 0)[:wq.shape[0]])))
+    ref, mag = x @ w.T, x.abs() @ w.abs().T
+    if r is not None:
+        ref, mag = ref + r.double(), mag + r.double().abs()
+    bound = mag * R.product_bound(R.blocks(xq.shape[1]), 1)
+    if y.dtype == torch.bfloat16:
+        bound = bound + (ref.abs() + bound) * 2.0 ** -8
+    off = (y.double() - ref).abs()
+    assert (off <= bound).all(), float((off / bound.clamp_min(1e-300)).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,N,K", [(4096, 6144, 2048), (3001, 5128, 1168)])
+def test_matmul_several_tiles_a_pair(colimoe, dtype, T, N, K):
+    # five whole tiles a pair and more, onto a residual (whose copies are asked for while a tile's sums are formed) and alone
+    for residual in (True, False):
+        xq, xs, wq, s, r = device_inputs(T, N, K, dtype, residual, T)
+        y = torch.full((T + 1, N), float("nan"), dtype=dtype, device="cuda")
+        ws = dense_ws(T, N, K)
+        B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, y, ws))
+        assert B.coli_moe_read_status(ws) == (B.COLI_OK, 0)
+        assert torch.isnan(y[T]).all()
+        check_matmul(y[:T], xq, xs, wq, s, r)
+
+
+def test_matmul_repeats_over_many_tiles(colimoe):
+    # 21 tiles a pair and operands that do not stay in L2: a tile that a step does not wait for is missing now and then
+    T, N, K = 16384, 6144, 2048
+    xq, xs, wq, s, r = device_inputs(T, N, K, torch.float32, True, 1)
+    ws = dense_ws(T, N, K)
+    want, y = (torch.empty(T, N, device="cuda") for _ in range(2))
+    B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, want, ws))
+    check_matmul(want[-600:], xq[-600:], xs[-600:], wq, s, r[-600:])
+    differ = []
+    for i in range(60):
+        y.fill_(float("nan"))
+        B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, y, ws))
+        differ.append((y != want).sum())
+    assert [int(d) for d in differ] == [0] * 60
+    assert B.coli_moe_read_status(ws) == (B.COLI_OK, 0)
