@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
     } else if (MODE != FP8_DENSE && warp < 8) {
         for (int i = tid; i < p.T * p.k; i += kEpi) {
             sm.t.pos[i] = position_of(p, i);
-            if (MODE == FP8_DOWN) sm.t.wt[i] = __ldg(p.wts + i);
+            if (MODE == FP8_DOWN) sm.t.wt[i] = p.wts[i];
         }
     }
     tc_fence_before();
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
 #pragma unroll
                     for (int i = 0; i < B; i++) {
                         const int k = min(kb + i, sg.k1 - 1);
-                        xv[i] = __ldg(xs + k);
+                        xv[i] = xs[k];
                         wv[i] = __ldg(ws + k);
                     }
                 };

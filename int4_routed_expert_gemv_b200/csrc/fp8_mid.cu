@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mid_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < B; i++) {
                     const int k = min(kb + i, it.kb1 - 1);
-                    xv[i][0] = __ldg(xs[0] + k);
-                    xv[i][1] = __ldg(xs[1] + k);
+                    xv[i][0] = xs[0][k];
+                    xv[i][1] = xs[1][k];
                     av[i] = __ldg(w0 + k);
                     bv[i] = __ldg(w1 + k);
                 }

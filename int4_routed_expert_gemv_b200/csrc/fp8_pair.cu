@@ -470,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float* wb = MODE == FP8_GATE_UP ? wa + (size_t)nb * p.kb : 2 * w.rb + 1 < nb ? wa + p.kb : wa;
             if (p.kb % 4 == 0) {
                 // a row's four in one load: 32 rows a warp are 32 accesses either way
-                const float4 x = __ldg(reinterpret_cast<const float4*>(xs + kb));
+                const float4 x = *reinterpret_cast<const float4*>(xs + kb);
                 const float4 a = __ldg(reinterpret_cast<const float4*>(wa + kb));
                 const float4 b = __ldg(reinterpret_cast<const float4*>(wb + kb));
                 xn[0] = x.x, xn[1] = x.y, xn[2] = x.z, xn[3] = x.w;
@@ -480,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int k = min(kb + i, p.kb - 1);
-                    xn[i] = __ldg(xs + k);
+                    xn[i] = xs[k];
                     an[i] = __ldg(wa + k);
                     bn[i] = __ldg(wb + k);
                 }

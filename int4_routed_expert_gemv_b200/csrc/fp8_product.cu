@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(256) fp8_gather_kernel(int positions, int k, i
         const int t = in ? a / k : 0;
         if (!in && lane == 0) set_flag(status, DEV_BAD_INDEX);
         for (int c = lane; c < pieces; c += 32)
-            to[(size_t)p * pieces + c] = in ? __ldg(x + (size_t)t * pieces + c) : make_uint4(0, 0, 0, 0);
-        for (int c = lane; c < kb; c += 32) to_s[(size_t)p * kb + c] = in ? __ldg(xs + (size_t)t * kb + c) : 0.0f;
+            to[(size_t)p * pieces + c] = in ? x[(size_t)t * pieces + c] : make_uint4(0, 0, 0, 0);
+        for (int c = lane; c < kb; c += 32) to_s[(size_t)p * kb + c] = in ? xs[(size_t)t * kb + c] : 0.0f;
     }
 }
 

@@ -338,7 +338,10 @@ inline cudaError_t allow_smem(size_t bytes)
 }
 
 // Launch that may begin while the kernel before it in the stream ends: its set-up then costs
-// no time of its own.  Kernels launched so wait (pdl_wait) before they touch memory.
+// no time of its own.  Kernels launched so wait (pdl_wait) before they touch memory, and read what a call
+// is given with ordinary loads: the read-only path (__ldg) is for memory that nothing writes while
+// the kernel runs, which these already do while the kernel before writes.  Only weights, laid out
+// long before, go through it.
 template <auto Kernel, class... A>
 inline cudaError_t launch_early(int grid, int threads, size_t smem, cudaStream_t s, const A&... args)
 {

@@ -110,3 +110,10 @@ def test_the_pairs_mmas_wait_for_their_tiles():
     for n in stages:
         assert not issued_too_early(n, order), (n, order)
     assert issued_too_early(3, ["full", "acc_empty"]), "the model knows the other order's fault"
+
+
+@pytest.mark.parametrize("name", KERNELS + ["fp8_product.cu"])
+def test_only_weights_go_through_the_read_only_path(name):
+    # the kernel before may still write everything else when these begin
+    for arg in re.findall(r"__ldg\(((?:[^()]|\([^()]*\))*)\)", source(name)):
+        assert re.match(r"(reinterpret_cast<const float4\*>\()?w[sab01] \+ k", arg), arg

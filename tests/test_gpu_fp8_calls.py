@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import fp8ref as R
+import test_gpu_fp8 as F
 from int4_routed_expert_gemv_b200 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +91,45 @@ def test_matmul_repeats_over_many_tiles(colimoe):
         differ.append((y != want).sum())
     assert [int(d) for d in differ] == [0] * 60
     assert B.coli_moe_read_status(ws) == (B.COLI_OK, 0)
+
+
+@pytest.mark.parametrize("T,H,E", [(3, 1024, 8), (40, 1088, 16), (150, 512, 4), (600, 1024, 6)])
+def test_other_inputs_call_after_call(colimoe, T, H, E):
+    # norm and experts on two batches in turn, through the same buffers and workspace and with nothing in between: what
+    # one kernel writes the next, which begins before it ends, has to read
+    c = F.Case(H, 320, E, 2, 1, T, seed=T)
+    g = torch.Generator().manual_seed(3)
+    xs = [torch.randn(T, H, generator=g).cuda() * m for m in (1, 40)]
+    q, s = torch.empty(T, H, dtype=R.E4M3, device="cuda"), torch.empty(T, R.blocks(H), device="cuda")
+    wq, wsc = (t.cuda() for t in R.weights(264, H, g))
+    y, z = torch.empty(T, H, device="cuda"), torch.empty(T, 264, device="cuda")
+    gammas = [torch.randn(H, generator=g).cuda() for _ in range(2)]
+    w, zws = c.w.cuda(), dense_ws(T, 264, H)
+
+    def step(j):
+        B.check(B.coli_rmsnorm_fp8(H, T, xs[j], None, gammas[j], 1e-6, None, None, q, s))
+        B.check(B.coli_moe_gate_up_fp8(c.dims, c.weights, q, s, T, *c.dl, c.hq, c.hs, c.ws))
+        B.check(B.coli_moe_forward_fp8(c.dims, c.weights, q, s, T, w, *c.dl, xs[j], y, c.ws))
+        B.check(B.coli_fp8_matmul(T, 264, H, q, s, wq, wsc, None, z, zws))
+
+    want = []
+    for j in range(2):
+        step(j)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (c.hq, c.hs, y, z)])
+    for i in range(40):
+        step(i % 2)
+        step((i + 1) % 2)
+        for a, b in zip((c.hq, c.hs, y, z), want[(i + 1) % 2]):
+            assert torch.equal(a, b)
+    # the two batches' products one behind the other, without the norm
+    qs = []
+    for j in range(2):
+        B.check(B.coli_rmsnorm_fp8(H, T, xs[j], None, gammas[j], 1e-6, None, None, q, s))
+        qs.append((q.clone(), s.clone()))
+    outs = [(torch.full_like(c.hq, 0x55), torch.full_like(c.hs, -7.0)) for _ in range(20)]
+    for i, (hq, hs) in enumerate(outs):
+        B.check(B.coli_moe_gate_up_fp8(c.dims, c.weights, *qs[i % 2], T, *c.dl, hq, hs, c.ws))
+    for i, (hq, hs) in enumerate(outs):
+        assert torch.equal(hq, want[i % 2][0]) and torch.equal(hs, want[i % 2][1])
+    assert B.coli_moe_read_status(c.ws) == (B.COLI_OK, 0)
