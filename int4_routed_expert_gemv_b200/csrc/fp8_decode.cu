@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
                             sc[m][j + 3] = f.w;
                         }
                     const uint32_t mask = MODE == FP8_DOWN ? sm.mask[s] >> (wg * C) : 0xFFu;
-                    tmem_wait_ld();
+                    tmem_wait_ld(v[0], v[1]);
 #pragma unroll
                     for (int m = 0; m < 2; m++)
 #pragma unroll

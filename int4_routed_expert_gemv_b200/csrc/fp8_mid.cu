@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mid_kernel(const __grid_const
 #pragma unroll
                         for (int j = 0; j < 4; j++)
                             f[j] = *reinterpret_cast<const float4*>(&sm.scale[s][m][wg * C + c0 + 4 * j]);
-                        tmem_wait_ld();
+                        tmem_wait_ld(v);
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
                             float* a = &acc[m][c0 + 4 * j];

@@ -573,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_ld16(ta, v[0]);
 #pragma unroll
                         for (int c = 0; c < 8; c++) {
-                            tmem_wait_ld();
+                            tmem_wait_ld(v[c & 1]);
                             if (c < 7) tmem_ld16(ta + (c + 1) * 16 + (c >= 3 ? 64 : 0), v[(c + 1) & 1]);
                             else {
                                 tc_fence_before();

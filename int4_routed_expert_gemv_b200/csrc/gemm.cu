@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
                         my_w = p.w[a];
                     }
                 }
-                tmem_wait_ld();
+                tmem_wait_ld(g);
+                if (phase == 0) tmem_wait_ld(u);
 #pragma unroll
                 for (int j = 0; j < 16; j++) {            // unrolled: g, u stay in registers
                     if (j >= nc) break;

@@ -117,3 +117,10 @@ def test_only_weights_go_through_the_read_only_path(name):
     # the kernel before may still write everything else when these begin
     for arg in re.findall(r"__ldg\(((?:[^()]|\([^()]*\))*)\)", source(name)):
         assert re.match(r"(reinterpret_cast<const float4\*>\()?w[sab01] \+ k", arg), arg
+
+
+@pytest.mark.parametrize("name", KERNELS + ["gemm.cu"])
+def test_waits_for_tensor_memory_name_what_was_loaded(name):
+    # the registers of a load are valid after the wait only, which the compiler learns from the operands alone
+    waits = re.findall(r"tmem_wait_ld\(([^)]*)\)", source(name))
+    assert waits and all(waits)
