@@ -286,7 +286,8 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
 // c = -g - t ln 2 is what the rounding of t left out (one FMA, nearly exact, as its terms nearly cancel; c^2 is
 // far below a rounding).  The quotient is an approximate reciprocal's with one correction by its
 // remainder, as Quantizer's.  With g held to -88 the denominator stays finite, and from 2^126 on its
-// reciprocal is flushed to 0, which the quotient is to within 2^-119.
+// reciprocal is flushed to 0, which the quotient is to within 2^-119.  An infinite g is its own quotient, whose
+// remainder, inf - inf, has to stay out of it: fminf passes the NaN over.
 __device__ __forceinline__ float swiglu(float g, float u)
 {
     const float x = fminf(fmaxf(g, -88.0f), 200.0f);
@@ -296,7 +297,7 @@ __device__ __forceinline__ float swiglu(float g, float u)
     const float d = 1.0f + fmaf(e, c, e);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     const float q = g * r;
-    return fmaf(fmaf(-q, d, g), r, q) * u;
+    return fmaf(fminf(fmaf(-q, d, g), 3.4028235e38f), r, q) * u;
 }
 
 // One thread, after its CTA's barrier: counts a part of a tile whose sums the CTA has stored.

@@ -133,3 +133,48 @@ def test_other_inputs_call_after_call(colimoe, T, H, E):
     for i, (hq, hs) in enumerate(outs):
         assert torch.equal(hq, want[i % 2][0]) and torch.equal(hs, want[i % 2][1])
     assert B.coli_moe_read_status(c.ws) == (B.COLI_OK, 0)
+
+
+@pytest.mark.parametrize("T", [4, 40, 300])
+def test_a_gate_that_overflows(colimoe, T):
+    # every kernel: silu(+inf) * u is an infinity of u's sign, which takes its block's scale with it and no other value
+    H, I, E = 1024, 192, 4
+    G = torch.zeros(I, H, dtype=torch.uint8)
+    U = torch.zeros(I, H, dtype=torch.uint8)
+    G[0, 0], G[1, 0], G[130, 0] = 0x7E, 0x01, 0x7E             # 448, 2^-9, 448
+    U[0, 0], U[1, 0], U[130, 0] = 0x38, 0x38, 0x38             # 1
+    U[0, 1] = 0xFE                                             # -448
+    sc = [torch.ones(2, 8), torch.ones(2, 8), torch.ones(8, 2)]
+    sc[0][0], sc[0][1] = 1e38, 2.0 ** -20
+    sc[1][:] = 2.0 ** -20
+    blob = torch.cat([G.reshape(-1), U.reshape(-1), torch.zeros(H * I, dtype=torch.uint8)] +
+                     [t.reshape(-1).view(torch.uint8) for t in sc])
+    stride = (blob.numel() + 255) // 256 * 256
+    experts = torch.zeros(E, stride, dtype=torch.uint8)
+    experts[0, :blob.numel()] = blob
+    experts = experts.cuda()
+    dims, weights = B.make_dims(H, I, E, 1, 0), B.make_weights(None, None, experts, None, stride)
+    lst = [t.cuda() for t in R.lists(torch.zeros(T, 1, dtype=torch.int32), E)]
+    ws = torch.zeros(B.coli_moe_workspace_bytes_fp8(dims, T), dtype=torch.uint8, device="cuda")
+    B.check(B.coli_moe_workspace_init(ws))
+    x = torch.zeros(T, H, dtype=torch.uint8)
+    x[:, 0] = 0x7E
+    x[2, 1] = 0x7E                                             # u of row 0 negative
+    x[3, 0] = 0x7F                                             # a NaN of its own
+    xs = torch.ones(T, 8)
+    xs[1] = xs[4:] = 2.0 ** -60                                # these gates stay finite
+    hq, hs = torch.full((T, I), 0x55, dtype=torch.uint8, device="cuda"), torch.empty(T, 2, device="cuda")
+    B.check(B.coli_moe_gate_up_fp8(dims, weights, x.cuda(), xs.cuda(), T, *lst, hq, hs, ws))
+    assert B.coli_moe_read_status(ws) == (B.COLI_OK, 0)
+    hq, hs = hq.cpu(), hs.cpu()
+    inf = float("inf")
+    for t in (0, 2):
+        assert hs[t, 0] == inf and hq[t, 0] & 0x7F == 0x7F, t
+        assert (hq[t, 1:128] & 0x7F == 0).all(), t
+    g, u = 448 * 448 * 2.0 ** -20, 448 * 2.0 ** -20            # the second block of token 0
+    h = g / (1 + 2.718281828459045 ** -g) * u
+    assert abs(float(hs[0, 1]) * 448 - h) <= h * 20 * R.U32 and hq[0, 130] == 0x7E
+    assert torch.isnan(hs[3, 0]) and (hq[3, :128] & 0x7F == 0x7F).all()
+    for t in [1] + list(range(4, T)):
+        h = 448 * 448 * 1e38 * 2.0 ** -60 * (448 * 2.0 ** -80)
+        assert abs(float(hs[t, 0]) * 448 - h) <= h * 20 * R.U32 and hq[t, 0] == 0x7E, t
