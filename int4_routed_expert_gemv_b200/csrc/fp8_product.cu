@@ -107,18 +107,30 @@ __global__ void __launch_bounds__(256) fp8_clear_kernel(size_t n, uint4* p)
 }
 
 // Rows of x and their scales in list order: row p is token assign[p] / k.  Positions that are none
-// of the batch's are flagged and get zeros.
+// of the batch's are flagged and get zeros.  Copied are the rows up to the largest end of a list that the product takes
+// (read_groups), whatever the lists behind it say: it may read no row that an earlier call left here.
 __global__ void __launch_bounds__(256) fp8_gather_kernel(int positions, int k, int E, int pieces, int kb,
                                                          const int32_t* n_union, const int32_t* offsets,
                                                          const int32_t* assign, const uint4* x, const float* xs, uint4* to,
                                                          float* to_s, uint32_t* status)
 {
+    __shared__ int end;
+    const int warps = gridDim.x * 8, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) end = 0;
     pdl_launch_dependents();
     pdl_wait();
-    const int nu = min(max(*n_union, 0), E);
-    const int rows = min(max(offsets[nu], 0), positions);
+    const int nu = *n_union;
+    int most = 0;
+    for (int u = threadIdx.x; u < E; u += 256) {
+        const int b = offsets[u], e = offsets[u + 1];
+        if (u < nu && b >= 0 && e >= b && e <= positions) most = max(most, e);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    __syncthreads();
+    if (lane == 0) atomicMax(&end, most);
+    __syncthreads();
+    const int rows = end;
     // a warp a row
-    const int warps = gridDim.x * 8, lane = threadIdx.x & 31;
     for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < rows; p += warps) {
         const int a = assign[p];
         const bool in = a >= 0 && a < positions;

@@ -178,3 +178,97 @@ def test_a_gate_that_overflows(colimoe, T):
     for t in [1] + list(range(4, T)):
         h = 448 * 448 * 1e38 * 2.0 ** -60 * (448 * 2.0 ** -80)
         assert abs(float(hs[t, 0]) * 448 - h) <= h * 20 * R.U32 and hq[t, 0] == 0x7E, t
+
+
+# ------------------------------------------------------------------------------------------------
+# lists
+# ------------------------------------------------------------------------------------------------
+def taken(c, lst):
+    """What the calls take of any lists: (matrices, rows, positions) of each list that lies within the batch, and of
+    those the positions that are the batch's; the shared expert last."""
+    union, n, off, asg = (t.tolist() for t in lst)
+    P, out = c.T * c.L.k, []
+    for u in range(min(max(n[0], 0), c.L.E)):
+        if 0 <= union[u] < c.L.E and 0 <= off[u] <= off[u + 1] <= P:
+            at = [p for p in range(off[u], off[u + 1]) if 0 <= asg[p] < P]
+            out.append((c.L.mats[union[u]], torch.tensor(at, dtype=torch.long),
+                        torch.tensor([asg[p] for p in at], dtype=torch.long)))
+    if c.L.n_shared:
+        out.append((c.L.mats[c.L.E], torch.arange(P, P + c.T), None))
+    return out
+
+
+def check_lists(c, lst, monkeypatch, status, zeros=()):
+    """Both products over any lists, against 64 bits.  zeros: positions whose row of h may be zeros."""
+    with monkeypatch.context() as m:
+        m.setattr(R, "groups", lambda L, l, T: taken(c, lst))
+        dl = [t.cuda() for t in lst]
+        n, I = c.rows, c.L.I
+        # another batch first: nothing of it may be left in what the next call reads
+        B.check(B.coli_moe_gate_up_fp8(c.dims, c.weights, c.xq.flip(0).cuda(), (c.xs * 3).cuda(), c.T, *c.dl, c.hq, c.hs,
+                                       c.ws))
+        B.check(B.coli_moe_workspace_init(c.ws))
+        c.hq.fill_(0x55)
+        c.hs.fill_(-7.0)
+        B.check(B.coli_moe_gate_up_fp8(c.dims, c.weights, c.xq.cuda(), c.xs.cuda(), c.T, *dl, c.hq, c.hs, c.ws))
+        assert B.coli_moe_read_status(c.ws) == status
+        hq, hs = c.hq.cpu(), c.hs.cpu()
+        h, err, named = R.gate_up(c.L, c.xq, c.xs, lst)
+        left = torch.cat([~named, torch.ones(1, dtype=torch.bool)])
+        for p in zeros:
+            assert not named[p]
+            assert (hq[p] == 0x55).all() and (hs[p] == -7).all() or (hq[p] & 0x7F == 0).all() and (hs[p] == 0).all()
+            left[p] = False
+        assert (hq[left] == 0x55).all() and (hs[left] == -7.0).all(), "rows outside the lists were written"
+        q, s, h, err = hq[:n][named].view(R.E4M3), hs[:n][named], h[named], err[named]
+        sd = s.double().repeat_interleave(128, 1)[:, :I]
+        bound = err + (h.abs() + err) * 2.0 ** -4 * (1 + 2.0 ** -20) + sd * 2.0 ** -10
+        assert ((R.dequant(q, s) - h).abs() <= bound).all()
+        top = torch.nn.functional.pad(h.abs(), (0, s.shape[1] * 128 - I)).view(h.shape[0], -1, 128).amax(2)
+        terr = torch.nn.functional.pad(err, (0, s.shape[1] * 128 - I)).view(h.shape[0], -1, 128).amax(2)
+        assert ((s.double() - top / 448).abs() <= terr / 448 + top / 448 * 2 * R.U32).all()
+
+        hq, hs = R.activations(n, I, torch.Generator().manual_seed(77))
+        hq.view(torch.uint8)[~named] = 0x7F          # rows that the lists leave out are not read
+        B.check(B.coli_moe_workspace_init(c.ws))
+        c.y.fill_(float("nan"))
+        B.check(B.coli_moe_down_fp8(c.dims, c.weights, hq.cuda(), hs.cuda(), c.T, c.w.cuda(), *dl, c.res.cuda(), c.y, c.ws))
+        assert B.coli_moe_read_status(c.ws) == status
+        ref, bound = R.down(c.L, hq, hs, c.w, lst, c.res)
+        assert ((c.y[:c.T].cpu().double() - ref).abs() <= bound).all()
+        assert torch.isnan(c.y[c.T:]).all()
+
+
+# of 6 experts, 2 each: the 16-token kernel, the 64-token one and the pairs, in both products
+LIST_SIZES = [(3, 256), (40, 1024), (300, 256)]
+
+
+@pytest.mark.parametrize("T,H", LIST_SIZES)
+@pytest.mark.parametrize("bad", ["expert", "offset", "assign", "count", "tail"])
+def test_bad_lists_leave_the_others_right(colimoe, monkeypatch, T, H, bad):
+    c = F.Case(H, 192, 6, 2, 1, T, seed=8)
+    u, m, o, a = [t.clone() for t in c.lst]
+    zeros = ()
+    if bad == "expert":
+        u[0] = 1 << 20
+    elif bad == "offset":
+        o[1] = 1 << 20
+    elif bad == "assign":
+        a[0], a[1] = -5, 1 << 30
+        zeros = (0, 1)
+    elif bad == "count":
+        m[0] = 1 << 20
+    else:      # the last list ends before the ones in front of it
+        assert int(m[0]) >= 3 and int(o[2]) > 1
+        m[0], o[3] = 3, 1
+    check_lists(c, (u, m, o, a), monkeypatch, (B.COLI_EDEVICE, B.DEV_BAD_INDEX), zeros)
+
+
+@pytest.mark.parametrize("T,H", LIST_SIZES)
+def test_lists_of_one_rank_in_every_kernel(colimoe, monkeypatch, T, H):
+    # experts 2 .. 4 of 6: some tokens have none of them, some slots are left out; then no expert at all
+    c = F.Case(H, 192, 6, 2, 1, T, seed=6, e0=2, e1=5)
+    check_lists(c, c.lst, monkeypatch, (B.COLI_OK, 0))
+    none = (torch.full((3,), -1, dtype=torch.int32), torch.tensor([0], dtype=torch.int32), torch.zeros(4, dtype=torch.int32),
+            c.lst[3])
+    check_lists(c, none, monkeypatch, (B.COLI_OK, 0))
