@@ -322,8 +322,10 @@ COLI_API coli_status coli_rmsnorm(int32_t hidden, int32_t T, const float* x, con
  * (colibri README.zh-CN "开始使用 / 2. 获取模型").
  * The fp8 calls share one kind of workspace among themselves; init it with
  * coli_moe_workspace_init, read errors with coli_moe_read_status (COLI_DEV_BAD_INDEX: lists
- * outside the batch, whose names are neither read nor written, or, for T <= 16, a list that
- * names a token twice, of which one position counts; larger batches add every one), and keep calls
+ * outside the batch, whose names are neither read nor written (above 16 tokens a row of h whose
+ * assign entry is none of the batch's becomes zeros); for T <= 16, a list that names a token twice, of
+ * which one position counts, where larger batches add every one; in the second product, and for T <= 16 in both,
+ * an assign entry that stands twice in the lists, whose token's y is then undefined), and keep calls
  * that use one workspace in one order (one stream, or events between streams). */
 
 /* Residual addition, RMSNorm and quantisation in one pass:

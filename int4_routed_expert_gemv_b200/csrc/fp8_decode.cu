@@ -57,6 +57,7 @@ struct Tables {
     Groups<kMaxGroups> g;
     int pos[kMaxPos];                   // t * k + slot of each list position (-1: not of this batch)
     float wt[kMaxPos];                  // routing weights [t * k + slot]
+    uint32_t named[kMaxPos / 32];       // positions that the lists have named (bits)
 };
 
 struct Smem {
@@ -456,14 +457,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_decode_kernel(const __grid_co
             }
         }
     } else if (MODE != FP8_DENSE && blockIdx.x == 0) {
-        // warp 11: list positions that are none of the batch's, or whose token the list names again
+        // warp 11: list positions that are none of the batch's or are named again, or whose token the list names again
         bool bad = false;
+        if (lane < kMaxPos / 32) sm.t.named[lane] = 0;
+        __syncwarp();
         for (int g = p.n_shared + lane; g < ng; g += 32) {
             const int count = sm.t.g.count[g], base = sm.t.g.base[g];
             bad |= count > p.T;
             for (int l = 0; l < min(count, p.T); l++) {
                 const int a = sm.t.pos[base + l];
-                bad |= a < 0;
+                if (a < 0) bad = true;
+                else bad |= atomicOr(&sm.t.named[a / 32], 1u << a % 32) >> a % 32 & 1;
                 for (int i = l + 1; i < min(count, p.T); i++) bad |= a / p.k == sm.t.pos[base + i] / p.k;
             }
         }

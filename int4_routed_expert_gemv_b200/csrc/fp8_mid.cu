@@ -235,11 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_mid_kernel(const __grid_const
             while (sch.next(it)) {
                 const Tile tl = look_up(it.tile);
                 if (tl.rb != 0 || it.kb0 != 0 || tl.g.expert < 0) continue;
-                for (int j = lane; j < tl.n; j += 32) {
-                    const int pos = tl.g.base + tl.t0 + j, a = position_of(p, pos);
-                    if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                    else p.z_row[a] = pos + 1;
-                }
+                for (int j = lane; j < tl.n; j += 32) place_row(p, tl.g.base + tl.t0 + j);
             }
     } else {
         // ------------------------- scaled accumulation, outputs -------------------------

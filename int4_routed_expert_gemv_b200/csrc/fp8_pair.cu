@@ -433,12 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (MODE == FP8_DOWN && more && tl.rb == 0 && it.kb0 == 0 && tl.g.expert >= 0)
-                    // where the combine finds the rows of z
-                    for (int j = rank * kM + lane; j < min(tl.n, (rank + 1) * kM); j += 32) {
-                        const int pos = tl.g.base + tl.t0 + j, a = position_of(p, pos);
-                        if (a < 0) set_flag(p.status, DEV_BAD_INDEX);
-                        else p.z_row[a] = pos + 1;
-                    }
+                    for (int j = rank * kM + lane; j < min(tl.n, (rank + 1) * kM); j += 32) place_row(p, tl.g.base + tl.t0 + j);
             }
         }
     } else {

@@ -147,6 +147,14 @@ __device__ __forceinline__ int position_of(const Params& p, int pos)
     return a < 0 || a >= p.T * p.k ? -1 : a;
 }
 
+// DOWN above 16 tokens: where the combine finds row `pos` of z.  A position that the lists name again is flagged, and
+// the last one counts, whatever the order.
+__device__ __forceinline__ void place_row(const Params& p, int pos)
+{
+    const int a = position_of(p, pos);
+    if (a < 0 || atomicMax(&p.z_row[a], pos + 1) != 0) set_flag(p.status, DEV_BAD_INDEX);
+}
+
 struct Item {
     int tile, kb0, kb1, slice;
 };

@@ -272,3 +272,32 @@ def test_lists_of_one_rank_in_every_kernel(colimoe, monkeypatch, T, H):
     none = (torch.full((3,), -1, dtype=torch.int32), torch.tensor([0], dtype=torch.int32), torch.zeros(4, dtype=torch.int32),
             c.lst[3])
     check_lists(c, none, monkeypatch, (B.COLI_OK, 0))
+
+
+@pytest.mark.parametrize("T,H", LIST_SIZES)
+@pytest.mark.parametrize("where", ["one list", "two lists"])
+def test_a_position_named_twice_is_flagged(colimoe, T, H, where):
+    c = F.Case(H, 192, 6, 2, 1, T, seed=8)
+    a, off = c.lst[3].clone(), c.lst[2].tolist()
+    # the first entry of a list in place of the last of the same list, or of the last list
+    n = int(c.lst[1][0])
+    u = max(range(n), key=lambda i: off[i + 1] - off[i])
+    first, last = (off[u], off[u + 1] - 1) if where == "one list" else (off[0], off[n] - 1)
+    assert first != last
+    twice = int(a[first])
+    a[last] = twice
+    lst = [c.dl[0], c.dl[1], c.dl[2], a.cuda()]
+    hq, hs = R.activations(c.rows, 192, torch.Generator().manual_seed(1))
+    ys = []
+    for _ in range(3):
+        B.check(B.coli_moe_workspace_init(c.ws))
+        B.check(B.coli_moe_down_fp8(c.dims, c.weights, hq.cuda(), hs.cuda(), T, c.w.cuda(), *lst, c.res.cuda(), c.y, c.ws))
+        assert B.coli_moe_read_status(c.ws) == (B.COLI_EDEVICE, B.DEV_BAD_INDEX)
+        ys.append(c.y.clone())
+    assert torch.equal(ys[0][:T], ys[1][:T]) and torch.equal(ys[0][:T], ys[2][:T])
+    # tokens that neither entry belongs to are right
+    ref, bound = R.down(c.L, hq, hs, c.w, c.lst, c.res)
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[[twice // 2, int(c.lst[3][last]) // 2]] = False
+    off_ = (ys[0][:T].cpu().double() - ref).abs()
+    assert (off_[keep] <= bound[keep]).all()
