@@ -139,6 +139,17 @@ def _dt(x: torch.Tensor) -> int:
     raise TypeError(f"unsupported activation dtype {x.dtype}")
 
 
+_F32 = torch.float32
+
+
+def _dt_same(x: torch.Tensor, a: Optional[torch.Tensor], b: Optional[torch.Tensor] = None) -> int:
+    """_dt(x), where the C call has one dtype for x, a and b: others would be read or written past their ends."""
+    d = x.dtype
+    if a is not None and a.dtype is not d or b is not None and b.dtype is not d:
+        raise TypeError(f"tensors of one type wanted, beside {d}")
+    return COLI_F32 if d is _F32 else _dt(x)
+
+
 def make_dims(hidden, inter, n_experts, top_k, n_shared=1) -> Dims:
     return Dims(hidden, inter, n_experts, top_k, n_shared)
 
@@ -282,7 +293,8 @@ def coli_rmsnorm(hidden, T, x, gamma, eps, out, stream=None) -> int:
 # The norm runs in few microseconds, so its marshalling is written out.
 
 def coli_rmsnorm_fp8(hidden, T, x, residual, gamma, eps, sum, out, q, scales, stream=None) -> int:
-    return lib().coli_rmsnorm_fp8(hidden, T, x.data_ptr(), None if residual is None else residual.data_ptr(), _dt(x),
+    return lib().coli_rmsnorm_fp8(hidden, T, x.data_ptr(), None if residual is None else residual.data_ptr(),
+                                  _dt_same(x, residual, sum),
                                   None if gamma is None else gamma.data_ptr(), eps,
                                   None if sum is None else sum.data_ptr(), None if out is None else out.data_ptr(),
                                   q.data_ptr(), scales.data_ptr(), _s(stream))
@@ -293,8 +305,8 @@ def coli_fp8_workspace_bytes(T: int, N: int, K: int) -> int:
 
 
 def coli_fp8_matmul(T, N, K, xq, xs, wq, wscales, residual, y, ws, stream=None) -> int:
-    return lib().coli_fp8_matmul(T, N, K, _p(xq), _p(xs), _p(wq), _p(wscales), _p(residual), _p(y), _dt(y), _p(ws),
-                                 ws.numel(), _s(stream))
+    return lib().coli_fp8_matmul(T, N, K, _p(xq), _p(xs), _p(wq), _p(wscales), _p(residual), _p(y),
+                                 _dt_same(y, residual), _p(ws), ws.numel(), _s(stream))
 
 
 def coli_moe_blob_bytes_fp8(hidden: int, inter: int) -> int:
