@@ -99,7 +99,8 @@ def _fp8_blocks(n: int) -> int:
 
 
 def quantize_matrix_fp8(W: np.ndarray):
-    """W [rows][cols] float -> (codes [rows][cols] uint8, scales [C(rows)][C(cols)] fp32)."""
+    """W [rows][cols] float -> (codes [rows][cols] uint8, scales [C(rows)][C(cols)] fp32).  A block with a NaN has a NaN
+    scale and NaN codes throughout; one with an infinity an infinite scale, NaN codes there and 0 elsewhere."""
     W = np.asarray(W, np.float32)
     rows, cols = W.shape
     rb, cb = _fp8_blocks(rows), _fp8_blocks(cols)
@@ -107,8 +108,9 @@ def quantize_matrix_fp8(W: np.ndarray):
     P[:rows, :cols] = W
     P = P.reshape(rb, FP8_BLOCK, cb, FP8_BLOCK)
     s = (np.abs(P).max(axis=(1, 3)) / np.float32(FP8_MAX)).astype(np.float32)
-    safe = np.where(s > 0, s, np.float32(1.0))
-    q = e4m3_codes(P / safe[:, None, :, None])
+    safe = np.where(s == 0, np.float32(1.0), s)
+    with np.errstate(invalid="ignore"):
+        q = e4m3_codes(P / safe[:, None, :, None])
     return np.ascontiguousarray(q.reshape(rb * FP8_BLOCK, cb * FP8_BLOCK)[:rows, :cols]), s
 
 
