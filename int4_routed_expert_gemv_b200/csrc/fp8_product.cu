@@ -3,6 +3,10 @@
 //
 //   out[t][n] = sum_b xs[t][b] * ws[n / 128][b] * sum_{c in block b} xq[t][c] * wq[n][c]
 //
+// xs * ws is formed first, in fp32, so that a term costs one FMA.  Where it is below 2^-126 it is off by up to
+// 2^-150 and a block's sum of codes, at most 128 * 448^2 < 2^25, times that: outputs are off by less than 2^-125 a
+// block, far below what a layer's values hold.
+//
 //   DENSE    y = round(residual + out)
 //   GATE_UP  row p of the union lists: h = silu(g) * u, then codes and scales of h
 //   DOWN     up to 16 tokens the combine is part of the product (fp8_decode.cu); above,

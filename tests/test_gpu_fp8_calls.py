@@ -301,3 +301,38 @@ def test_a_position_named_twice_is_flagged(colimoe, T, H, where):
     keep[[twice // 2, int(c.lst[3][last]) // 2]] = False
     off_ = (ys[0][:T].cpu().double() - ref).abs()
     assert (off_[keep] <= bound[keep]).all()
+
+
+# ------------------------------------------------------------------------------------------------
+# range
+# ------------------------------------------------------------------------------------------------
+def tiny(t, g):
+    """Scales 2^-85 .. 2^-60 in place of t's: products of two of them lie on both sides of 2^-126 and of 2^-149."""
+    return torch.ldexp(1 + torch.rand(t.shape, generator=g), torch.randint(-85, -60, t.shape, generator=g))
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 300, 1040), (40, 300, 1040), (300, 300, 1040), (300, 301, 528)])
+def test_scale_products_below_the_normal_numbers(colimoe, T, N, K):
+    # every kernel: beside the usual bound, 2^-125 for each block (and a denormal result's own rounding, one a block)
+    g = torch.Generator().manual_seed(T)
+    xq, xs = R.activations(T, K, g)
+    wq, s = R.weights(N, K, g)
+    xs, s = tiny(xs, g), tiny(s, g)
+    y = torch.empty(T, N, device="cuda")
+    B.check(B.coli_fp8_matmul(T, N, K, xq.cuda(), xs.cuda(), wq.cuda(), s.cuda(), None, y, dense_ws(T, N, K)))
+    x, w = R.dequant(xq, xs), R.dequant_w(wq, s)
+    bound = (x.abs() @ w.abs().T) * R.product_bound(R.blocks(K)) + R.blocks(K) * (2.0 ** -125 + 2.0 ** -149)
+    off = (y.cpu().double() - x @ w.T).abs()
+    assert (off <= bound).all(), float((off / bound).max())
+
+
+@pytest.mark.parametrize("T,H", LIST_SIZES)
+def test_scale_products_below_the_normal_numbers_down(colimoe, T, H):
+    c = F.Case(H, 192, 6, 2, 1, T, seed=8)
+    g = torch.Generator().manual_seed(T)
+    hq, hs = R.activations(c.rows, 192, g)
+    hs = torch.ldexp(1 + torch.rand(hs.shape, generator=g), torch.randint(-130, -100, hs.shape, generator=g))
+    B.check(B.coli_moe_down_fp8(c.dims, c.weights, hq.cuda(), hs.cuda(), T, c.w.cuda(), *c.dl, None, c.y, c.ws))
+    ref, bound = R.down(c.L, hq, hs, c.w, c.lst, None)
+    more = 3 * R.blocks(192) * (2.0 ** -125 + 2.0 ** -149)
+    assert ((c.y[:T].cpu().double() - ref).abs() <= bound + more).all()
