@@ -318,7 +318,8 @@ COLI_API coli_status coli_rmsnorm(int32_t hidden, int32_t T, const float* x, con
  * Products accumulate in fp32: the 128 terms of a scale block on the tensor cores, then
  * times the product of both scales (and of the routing weight, in the second experts' product of up to 16
  * tokens), block after block in a fixed order (split over several blocks of the
- * grid where there are few tiles; still one fixed order for given sizes and device).  That
+ * grid where that fills it better; still one fixed order for given sizes, lists and device, and with other
+ * lists, as with other sizes, another: a token's last bits may depend on the other tokens' experts).  That
  * product is one fp32 number: below 2^-126 it loses bits, which puts an output off by up to 2^-125 for each such
  * scale block, and beyond fp32's largest it is infinite, and outputs infinite or NaN.  The
  * format is that of the fp8 checkpoints which the int4 containers are converted from
