@@ -336,3 +336,66 @@ def test_scale_products_below_the_normal_numbers_down(colimoe, T, H):
     ref, bound = R.down(c.L, hq, hs, c.w, c.lst, None)
     more = 3 * R.blocks(192) * (2.0 ** -125 + 2.0 ** -149)
     assert ((c.y[:T].cpu().double() - ref).abs() <= bound + more).all()
+
+
+# ------------------------------------------------------------------------------------------------
+# tiles whose K steps are split between workers, which add the parts up
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("T,N,K,dtype,residual", [
+    (64, 38400, 2048, torch.float32, True),        # 150 tiles for 148 CTAs, all split
+    (130, 12801, 2064, torch.bfloat16, True),      # 153 tiles, ragged rows of y
+    (600, 6400, 2064, torch.float32, True),        # 75 tiles for 74 pairs
+    (600, 6400, 2048, torch.bfloat16, False),
+    (1100, 7688, 1808, torch.bfloat16, True),      # 155 tiles: 74 whole ones beside 81 in parts
+])
+def test_matmul_split_tiles(colimoe, T, N, K, dtype, residual):
+    xq, xs, wq, s, r = device_inputs(T, N, K, dtype, residual, T)
+    ws = dense_ws(T, N, K)
+    ys = [torch.full((T + 1, N), float("nan"), dtype=dtype, device="cuda") for _ in range(2)]
+    for y in ys:
+        B.check(B.coli_fp8_matmul(T, N, K, xq, xs, wq, s, r, y, ws))
+    assert B.coli_moe_read_status(ws) == (B.COLI_OK, 0)
+    check_matmul(ys[0][:T], xq, xs, wq, s, r)
+    assert torch.isnan(ys[0][T]).all() and torch.equal(ys[0][:T], ys[1][:T])
+
+
+@pytest.mark.parametrize("T,H,I,E", [(40, 4096, 2048, 9),       # 160 tiles for 148 CTAs in both products
+                                     (150, 4864, 2432, 3)])     # 76 tiles for 74 pairs in both
+def test_experts_split_tiles(colimoe, T, H, I, E):
+    c = F.Case(H, I, E, 2, 1, T, seed=4)
+    assert all(0 < n <= 256 for n in (c.lst[2][1:] - c.lst[2][:-1])[:E].tolist()) and int(c.lst[1]) == E
+    c.check_gate_up()
+    c.check_down()
+    c.check_down(in_place=True)
+
+
+@pytest.mark.parametrize("T,H,I,E", [(40, 1024, 192, 6), (300, 256, 192, 6), (150, 1024, 2432, 3)])
+def test_two_graphs_on_one_workspace_in_every_kernel(colimoe, T, H, I, E):
+    # replayed in turn, and each twice in a row
+    c = F.Case(H, I, E, 2, 1, T, seed=9)
+    hq, hs = (t.cuda() for t in R.activations(c.rows, I, torch.Generator().manual_seed(10)))
+    w, res, xq, xs = c.w.cuda(), c.res.cuda(), c.xq.cuda(), c.xs.cuda()
+
+    def up():
+        B.check(B.coli_moe_gate_up_fp8(c.dims, c.weights, xq, xs, T, *c.dl, c.hq, c.hs, c.ws))
+
+    def down():
+        B.check(B.coli_moe_down_fp8(c.dims, c.weights, hq, hs, T, w, *c.dl, res, c.y, c.ws))
+
+    c.check_gate_up()
+    up()
+    down()
+    want = c.hq.clone(), c.hs.clone(), c.y.clone()
+    graphs = []
+    for f in (up, down):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f()
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1), (1, 1, 0, 0)):
+        c.hq[:c.rows] = 0
+        c.hs[:c.rows] = 0
+        c.y[:T] = 0
+        for i in order:
+            graphs[i].replay()
+        assert torch.equal(c.hq, want[0]) and torch.equal(c.hs, want[1]) and torch.equal(c.y[:T], want[2][:T])
+    assert B.coli_moe_read_status(c.ws) == (B.COLI_OK, 0)
