@@ -54,13 +54,12 @@ constexpr uint32_t kTile = kM * 128;              // bytes of a CTA's tokens or 
 constexpr uint32_t kStage = 2 * kTile;
 constexpr int kBufs = 2;
 constexpr uint32_t kTmem = kBufs * 256;
-constexpr int kBox = 128;                         // rows of a token box
 constexpr int kLeast = 6;                         // K steps of a run at least
 constexpr int kJoin = 12;                         // what joining the parts of a tile costs, in K steps
 constexpr uint32_t kOutBox = 32 * 128;            // a warp's 32 rows of 128 bytes of output
 
-// Three stages are enough (two, three and four more gain nothing: what bounds the copies is the
-// shared memory they share with the MMA's reads), which leaves room for a tile's outputs.
+// DENSE and DOWN stage a tile's outputs, which leaves room for three stages; GATE_UP, which does not, has the four
+// that took least time (above).
 template <int MODE>
 struct Shape {
     static constexpr int kStages = MODE == FP8_GATE_UP ? 4 : 3;
@@ -188,11 +187,6 @@ __device__ __forceinline__ void scaled_add(float* acc, const uint32_t (&v)[16], 
     for (int j = 0; j < 16; j++) acc[j] = fmaf(__uint_as_float(v[j]), s, acc[j]);
 }
 
-__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
-{
-    tma_load_3d(dst, map, x, y, z, bar);
-}
-
 __device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, int z, const void* src)
 {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
@@ -227,7 +221,7 @@ __device__ __forceinline__ void ask_residual(const Params& p, int c0, int y0, ui
     mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
     for (int j = 0; j < Boxes<Y>::N; j++)
-        if (Boxes<Y>::column(c0, j) < p.rows) load_box(box + j * kOutBox, &p.res, Boxes<Y>::column(c0, j), y0, 0, bar);
+        if (Boxes<Y>::column(c0, j) < p.rows) tma_load_3d(box + j * kOutBox, &p.res, Boxes<Y>::column(c0, j), y0, 0, bar);
 }
 
 // A warp's 32 rows of outputs, one per thread, to rows from y0 of the map (rows and columns
@@ -361,10 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const CUtensorMap* xm = &p.x[MODE == FP8_GATE_UP ? shared : 0];
                 const int z = shared ? 0 : tl.g.expert;
                 const int r0 = MODE == FP8_GATE_UP ? tl.rb * kM + rank * p.I : (tl.rb * 2 + rank) * kM;
-                // token rows of each CTA, in boxes
-                const int n0 = min(tl.n, kM), n1 = tl.n - n0;
-                const int boxes = ((rank ? n1 : n0) + kBox - 1) / kBox;
-                const uint32_t bytes = 2 * kTile + (uint32_t)((n0 + kBox - 1) / kBox + (n1 + kBox - 1) / kBox) * kBox * 128;
+                const int n1 = max(tl.n - kM, 0);      // token rows of rank 1
+                const bool tokens = rank == 0 || n1 > 0;
+                const uint32_t bytes = (n1 > 0 ? 4 : 3) * kTile;
                 const int base = MODE == FP8_DENSE || (MODE == FP8_GATE_UP && shared) ? 0 : tl.g.base;
                 const int row0 = base + tl.t0 + rank * kM;
                 for (int kb = it.kb0; kb < it.kb1; kb++, n++) {
@@ -377,8 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t bar = map_to(&sm.full[s], 0);
                         if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], bytes);
                         pair_load_3d(st + kTile, wm, kb * 128, r0, z, bar);
-                        for (int b = 0; b < boxes; b++)
-                            pair_load_2d(st + b * kBox * 128, xm, kb * 128, row0 + b * kBox, bar);
+                        if (tokens) pair_load_2d(st, xm, kb * 128, row0, bar);
                     }
                     __syncwarp();
                 }

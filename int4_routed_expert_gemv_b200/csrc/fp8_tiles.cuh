@@ -1,5 +1,5 @@
-// Pieces shared by the two kernels of the e4m3 products (fp8_decode.cu, fp8_pair.cu): the
-// launch's parameters, groups of tokens, the schedule of tiles, tensor-core wrappers.
+// Pieces shared by the three kernels of the e4m3 products (fp8_decode.cu, fp8_mid.cu, fp8_pair.cu): the
+// launch's parameters, waits, groups of tokens, the schedule of tiles, tensor-core wrappers.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
