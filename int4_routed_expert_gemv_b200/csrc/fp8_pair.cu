@@ -483,8 +483,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (dead) {
                 // no brief any more: the same items, without tokens, since the other warps wait for this one
                 // at named barriers
-                w.left = w.rb = w.expert = w.xrow = w.y0 = 0;
-                w.orow = -1;
+                w.left = 0;
+                w.orow = -1;         // (the rest goes unread)
                 Schedule again;      // (made here: registers are dear)
                 again.init(sm.tiles, p.kb, (int)n_clusters(), (int)cluster_id(), kLeast, kJoin, p.slices);
                 return again.at((int)briefs - 1, w.it);
