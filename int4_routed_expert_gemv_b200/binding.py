@@ -139,17 +139,6 @@ def _dt(x: torch.Tensor) -> int:
     raise TypeError(f"unsupported activation dtype {x.dtype}")
 
 
-_F32 = torch.float32
-
-
-def _dt_same(x: torch.Tensor, a: Optional[torch.Tensor], b: Optional[torch.Tensor] = None) -> int:
-    """_dt(x), where the C call has one dtype for x, a and b: others would be read or written past their ends."""
-    d = x.dtype
-    if a is not None and a.dtype is not d or b is not None and b.dtype is not d:
-        raise TypeError(f"tensors of one type wanted, beside {d}")
-    return COLI_F32 if d is _F32 else _dt(x)
-
-
 def make_dims(hidden, inter, n_experts, top_k, n_shared=1) -> Dims:
     return Dims(hidden, inter, n_experts, top_k, n_shared)
 
@@ -290,11 +279,17 @@ def coli_rmsnorm(hidden, T, x, gamma, eps, out, stream=None) -> int:
 
 # 8-bit floating point path: codes are torch.float8_e4m3fn (or uint8) tensors, scales fp32.
 
-# The norm runs in few microseconds, so its marshalling is written out.
+# The stream's tensors (x, residual, sum; y, residual) have one dtype in the C calls: another one's would be read or
+# written past its end.  The norm runs in few microseconds, so its marshalling is written out.
+_F32 = torch.float32
+
 
 def coli_rmsnorm_fp8(hidden, T, x, residual, gamma, eps, sum, out, q, scales, stream=None) -> int:
+    d = x.dtype
+    if residual is not None and residual.dtype is not d or sum is not None and sum.dtype is not d:
+        raise TypeError(f"x, residual and sum have one type, and x has {d}")
     return lib().coli_rmsnorm_fp8(hidden, T, x.data_ptr(), None if residual is None else residual.data_ptr(),
-                                  _dt_same(x, residual, sum),
+                                  COLI_F32 if d is _F32 else _dt(x),
                                   None if gamma is None else gamma.data_ptr(), eps,
                                   None if sum is None else sum.data_ptr(), None if out is None else out.data_ptr(),
                                   q.data_ptr(), scales.data_ptr(), _s(stream))
@@ -305,8 +300,10 @@ def coli_fp8_workspace_bytes(T: int, N: int, K: int) -> int:
 
 
 def coli_fp8_matmul(T, N, K, xq, xs, wq, wscales, residual, y, ws, stream=None) -> int:
-    return lib().coli_fp8_matmul(T, N, K, _p(xq), _p(xs), _p(wq), _p(wscales), _p(residual), _p(y),
-                                 _dt_same(y, residual), _p(ws), ws.numel(), _s(stream))
+    if residual is not None and residual.dtype is not y.dtype:
+        raise TypeError(f"residual and y have one type, not {residual.dtype} and {y.dtype}")
+    return lib().coli_fp8_matmul(T, N, K, _p(xq), _p(xs), _p(wq), _p(wscales), _p(residual), _p(y), _dt(y), _p(ws),
+                                 ws.numel(), _s(stream))
 
 
 def coli_moe_blob_bytes_fp8(hidden: int, inter: int) -> int:
