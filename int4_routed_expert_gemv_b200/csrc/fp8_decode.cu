@@ -28,8 +28,8 @@
 //
 // Bounded by reading the weights from HBM, and below some 100 MB by what a launch takes before the
 // first tile lands and after the last (lists, barriers, the first copies: 4 us; joining parts: 3 us).  Measured
-// back to back: GLM-shaped gate/up of one token 39.5 us (5.7 TB/s; no tile is split), of 16 tokens 135 us
-// (6.3 TB/s); down of one token 29 us (3.9 TB/s, every tile in 6 to 8 parts), of 16 78 us (5.5 TB/s); dense
+// back to back: GLM-shaped gate/up of one token 40 us (5.7 TB/s; no tile is split), of 16 tokens 135 us
+// (6.3 TB/s); down of one token 29 us (3.9 TB/s, every tile in 6 to 8 parts), of 16 82 us (5.1 TB/s); dense
 // 1 x 12288 x 6144 19 us (4.0 TB/s).
 #include <string.h>
 

@@ -6,7 +6,7 @@
 // and takes it less time than those take to arrive.  The pairs of fp8_pair.cu bring a CTA 16 KB a
 // step, and their step, 1000 cycles, is what 64 experts of 8 rows each waited for (GLM-shaped
 // gate/up of 64 tokens: 392 us, against 250 for reading the weights).  Here, bounded by those
-// reads: gate/up of 17 tokens 230 us (6.1 TB/s) and of 64 tokens 266 us (6.2 TB/s), dense 12288 x 6144 for
+// reads: gate/up of 17 tokens 236 us (6.0 TB/s) and of 64 tokens 272 us (6.0 TB/s), dense 12288 x 6144 for
 // 64 tokens 24 us (3.1 TB/s: 48 tiles of 48 K steps, joined once each).
 //
 // The columns of a tile are rows of one group, one after another: tokens (DENSE), or an expert's

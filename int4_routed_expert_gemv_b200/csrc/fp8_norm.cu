@@ -12,7 +12,7 @@
 // reduced across the CTA, and written out as sum, n, codes and scales.  16 neighbouring lanes
 // hold one scale block, so its maximum is four shuffles.  The scaling is done in pairs of
 // floats rather than doubles, whose conversions (16 a cycle and SM) cost more than the loads.
-// Measured: 8192 x 6144 with residual and out, bf16 91 us (6.1 TB/s), fp32 132 us (6.5 TB/s); codes alone, from
+// Measured: 8192 x 6144 with residual and out, bf16 91 us (6.1 TB/s), fp32 133 us (6.4 TB/s); codes alone, from
 // bf16, 71 us, where instructions bound (10 us of them the quantiser's); 4 rows 4 us, a launch's length.
 #include <cuda_bf16.h>
 

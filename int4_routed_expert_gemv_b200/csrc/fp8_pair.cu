@@ -30,12 +30,15 @@
 // A part of a split tile goes to the workspace; the last one to arrive adds the parts up in
 // K order (Schedule).
 //
-// Measured: 4096 x 4096 x 6144 to bf16 115 us (1.8 PFLOP/s), 16384 x 6144 x 2048 onto an fp32 residual 305 us,
-// GLM-shaped gate/up of 2048 tokens over 32 uneven lists 605 us (1.5 PFLOP/s of the tokens' products).  A K
-// step takes about 1000 cycles where the MMAs alone need 512: with the weights' copies left out 30 % less, with
-// one eighth of the accumulation 16 %, with none of its arithmetic 3 % less.  So the copies from L2 (32 KB a K
-// step and SM) bound it first, and more stages only make them wait for one another (GATE_UP with 3 / 4 / 5 / 6
-// stages: 625 / 607 / 613 / 620 us).
+// Measured in graphs of 30 calls: 4096 x 4096 x 6144 to bf16 117 us (1.8 PFLOP/s), 16384 x 6144 x 2048 onto an fp32
+// residual 310 to 340 us, GLM-shaped gate/up of 2048 tokens over 32 uneven lists 620 us (1.5 PFLOP/s of the tokens'
+// products); in loops of seconds, where the power limit holds the clock down, 139, 355 and 720 us.  No one resource is
+// used up (gate/up: the tensor pipe runs 42 % of the cycles, 39 % of the issue slots are taken, L2 is at 27 %).
+// Left out one at a time, in us of 117 / 310 / 620: the weights' copies 112 / 295 / 577, the tokens' 113 / 285 / 589,
+// the arithmetic of the accumulation 103 / 280 / 550, that and three quarters of its loads 101 / 280 / 519; for
+// the second also the copies out 271, the residual 264, both of bf16 and no residual 225.  So what bounds a K step is
+// the hand-over from MMA to accumulation and back, through two buffers that fill tensor memory, and where the
+// outputs are wide their copies add to it.  (GATE_UP with 3 / 4 / 5 / 6 stages: 625 / 607 / 613 / 620 us.)
 #include <string.h>
 
 #include <type_traits>
