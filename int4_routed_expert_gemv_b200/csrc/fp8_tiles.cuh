@@ -63,21 +63,6 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
-// Waits of one thread and of a whole warp.  After one that gives up (`dead`) nothing is waited for any
-// more, while the loops go on through every item, so that hand-overs still match.  In the warp's form, where each
-// lane polls for itself, the vote makes `dead` one answer and brings the lanes together again: the
-// tensor memory loads behind it want a converged warp.
-__device__ __forceinline__ void lane_wait(bool& dead, uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t site)
-{
-    if (!dead) dead = !mbar_wait(bar, parity, status, site);
-}
-
-__device__ __forceinline__ void warp_wait(bool& dead, uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t site)
-{
-    const bool ok = !dead && mbar_wait(bar, parity, status, site);
-    dead = !__all_sync(0xffffffffu, ok);
-}
-
 // One thread: until the last copies that it sent into a ring of stages have landed.
 __device__ __forceinline__ void drain(uint64_t* full, uint32_t stages, uint32_t sent, uint32_t* status, uint32_t site)
 {

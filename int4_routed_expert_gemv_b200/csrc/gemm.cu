@@ -358,8 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
             const Task tk = p.tasks[t];
             const SegView sv = seg_view(p, tk.seg);
             const int buf = tcount & 1;
-            if (!dead && !mbar_wait(&acc_full[buf], (tcount >> 1) & 1, p.status, kWaitSite + 7))
-                dead = true;
+            warp_wait(dead, &acc_full[buf], (tcount >> 1) & 1, p.status, kWaitSite + 7);
             tc_fence_after();
             const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)buf * 256u;
             const int grow = tk.rb * kRows + row;   // row of the weight matrix

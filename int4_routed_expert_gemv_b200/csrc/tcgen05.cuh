@@ -76,6 +76,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr));
 }
 
+// Waits of one thread and of a whole warp.  After one that gives up (`dead`) nothing is waited for any
+// more, while the loops go on through every item, so that hand-overs still match.  In the warp's form, where each
+// lane polls for itself, the vote makes `dead` one answer and brings the lanes together again: the
+// tensor memory loads behind it want a converged warp.
+__device__ __forceinline__ void lane_wait(bool& dead, uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t site)
+{
+    if (!dead) dead = !mbar_wait(bar, parity, status, site);
+}
+
+__device__ __forceinline__ void warp_wait(bool& dead, uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t site)
+{
+    const bool ok = !dead && mbar_wait(bar, parity, status, site);
+    dead = !__all_sync(0xffffffffu, ok);
+}
+
 // Until this thread's loads have returned, naming what they return: their registers hold the values only after the
 // wait, and without the operands nothing tells the compiler that arithmetic on them comes after it.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16])
