@@ -284,6 +284,18 @@ def coli_rmsnorm(hidden, T, x, gamma, eps, out, stream=None) -> int:
 _F32 = torch.float32
 
 
+def _s_for(x: torch.Tensor, stream):
+    """The stream's handle for a call on x, which has to lie on the stream's device: a kernel elsewhere would fault on it."""
+    at = x.get_device()
+    if at >= 0:
+        if stream is not None:
+            if getattr(stream, "device_index", at) == at:
+                return stream.cuda_stream
+        elif torch._C._cuda_getDevice() == at:
+            return torch._C._cuda_getCurrentRawStream(at)
+    raise ValueError(f"a tensor on {x.device}, and the call is not for that device")
+
+
 def coli_rmsnorm_fp8(hidden, T, x, residual, gamma, eps, sum, out, q, scales, stream=None) -> int:
     d = x.dtype
     if residual is not None and residual.dtype is not d or sum is not None and sum.dtype is not d:
@@ -292,7 +304,7 @@ def coli_rmsnorm_fp8(hidden, T, x, residual, gamma, eps, sum, out, q, scales, st
                                   COLI_F32 if d is _F32 else _dt(x),
                                   None if gamma is None else gamma.data_ptr(), eps,
                                   None if sum is None else sum.data_ptr(), None if out is None else out.data_ptr(),
-                                  q.data_ptr(), scales.data_ptr(), _s(stream))
+                                  q.data_ptr(), scales.data_ptr(), _s_for(x, stream))
 
 
 def coli_fp8_workspace_bytes(T: int, N: int, K: int) -> int:
@@ -303,7 +315,7 @@ def coli_fp8_matmul(T, N, K, xq, xs, wq, wscales, residual, y, ws, stream=None) 
     if residual is not None and residual.dtype is not y.dtype:
         raise TypeError(f"residual and y have one type, not {residual.dtype} and {y.dtype}")
     return lib().coli_fp8_matmul(T, N, K, _p(xq), _p(xs), _p(wq), _p(wscales), _p(residual), _p(y), _dt(y), _p(ws),
-                                 ws.numel(), _s(stream))
+                                 ws.numel(), _s_for(y, stream))
 
 
 def coli_moe_blob_bytes_fp8(hidden: int, inter: int) -> int:
@@ -318,21 +330,21 @@ def coli_moe_gate_up_fp8(dims, weights, xq, xs, T, union_ids, n_union, offsets, 
                          stream=None) -> int:
     return lib().coli_moe_gate_up_fp8(ctypes.byref(dims), ctypes.byref(weights), _p(xq), _p(xs), T, _p(union_ids),
                                       _p(n_union), _p(offsets), _p(assign), _p(hq), _p(hs), _p(ws), ws.numel(),
-                                      _s(stream))
+                                      _s_for(hq, stream))
 
 
 def coli_moe_down_fp8(dims, weights, hq, hs, T, w, union_ids, n_union, offsets, assign, residual, y, ws,
                       stream=None) -> int:
     return lib().coli_moe_down_fp8(ctypes.byref(dims), ctypes.byref(weights), _p(hq), _p(hs), T, _p(w),
                                    _p(union_ids), _p(n_union), _p(offsets), _p(assign), _p(residual), _p(y), _p(ws),
-                                   ws.numel(), _s(stream))
+                                   ws.numel(), _s_for(y, stream))
 
 
 def coli_moe_forward_fp8(dims, weights, xq, xs, T, w, union_ids, n_union, offsets, assign, residual, y, ws,
                          stream=None) -> int:
     return lib().coli_moe_forward_fp8(ctypes.byref(dims), ctypes.byref(weights), _p(xq), _p(xs), T, _p(w),
                                       _p(union_ids), _p(n_union), _p(offsets), _p(assign), _p(residual), _p(y),
-                                      _p(ws), ws.numel(), _s(stream))
+                                      _p(ws), ws.numel(), _s_for(y, stream))
 
 
 # ------------------------------------------------------------------------------------

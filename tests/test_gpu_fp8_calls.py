@@ -37,6 +37,8 @@ def test_matmul_of_several_seconds(colimoe):
     bound = ref * R.product_bound(n // 128)      # all terms are positive
     bound = bound + (ref + bound) * 2.0 ** -8
     got = y[rows][:, cols].cpu().double()
+    del codes, y
+    torch.cuda.empty_cache()
     assert ((got - ref).abs() <= bound).all()
 
 
