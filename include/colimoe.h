@@ -316,21 +316,25 @@ COLI_API coli_status coli_rmsnorm(int32_t hidden, int32_t T, const float* x, con
  * an infinity has a scale of NaN or infinity and NaN codes where its values were not finite
  * (every code of a block with a NaN).
  * Products accumulate in fp32: the 128 terms of a scale block on the tensor cores, then
- * times the product of both scales (and of the routing weight, in the second experts' product of up to 16
- * tokens), block after block in a fixed order (split over several blocks of the
- * grid where that fills it better; still one fixed order for given sizes, lists and device, and with other
- * lists, as with other sizes, another: a token's last bits may depend on the other tokens' experts).  That
- * product is one fp32 number: below 2^-126 it loses bits, which puts an output off by up to 2^-125 for each such
- * scale block, and beyond fp32's largest it is infinite, and outputs infinite or NaN.  The
- * format is that of the fp8 checkpoints which the int4 containers are converted from
+ * times the product of both scales (and of the routing weight, in the second experts' product
+ * of up to 16 tokens).  That product is one fp32 number: below 2^-126 it loses bits, which puts
+ * an output off by up to 2^-125 for each such scale block; beyond fp32's largest it is infinite,
+ * and outputs infinite or NaN.  Blocks are added one after another in a fixed order, split over
+ * several blocks of the grid where that fills it better: one order for given sizes, lists and
+ * device, and another for others, so a token's last bits may depend on the other tokens' experts.
+ * The format is that of the fp8 checkpoints which the int4 containers are converted from
  * (colibri README.zh-CN "开始使用 / 2. 获取模型").
  * The fp8 calls share one kind of workspace among themselves; init it with
- * coli_moe_workspace_init, read errors with coli_moe_read_status (COLI_DEV_BAD_INDEX: lists
- * outside the batch, whose names are neither read nor written (above 16 tokens a row of h whose
- * assign entry is none of the batch's becomes zeros); for T <= 16, a list that names a token twice, of
- * which one position counts, where larger batches add every one; in the second product, and for T <= 16 in both,
- * an assign entry that stands twice in the lists, whose token's y is then undefined), and keep calls
- * that use one workspace in one order (one stream, or events between streams). */
+ * coli_moe_workspace_init and keep calls that use one workspace in one order (one stream, or
+ * events between streams).  coli_moe_read_status reads errors:
+ *   COLI_DEV_BAD_INDEX  lists or positions outside the batch: their names are neither read nor
+ *                       written (above 16 tokens the row of h of such a position becomes zeros);
+ *                       for T <= 16 a list that names a token twice, of which one position
+ *                       counts (larger batches add every one); a position that stands twice in
+ *                       the lists (the second product, and for T <= 16 both), whose token's y is
+ *                       then undefined;
+ *   COLI_DEV_TIMEOUT    a wait gave up: the outputs are undefined, and the workspace has to be
+ *                       inited again, as its counters may be left over. */
 
 /* Residual addition, RMSNorm and quantisation in one pass:
  *   s = x + residual, rounded once to dtype (x itself without a residual);  sum = s;
