@@ -276,6 +276,15 @@ def test_lists_of_one_rank_in_every_kernel(colimoe, monkeypatch, T, H):
     check_lists(c, none, monkeypatch, (B.COLI_OK, 0))
 
 
+@pytest.mark.parametrize("T,H,E", [(500, 64, 300), (500, 1088, 300), (700, 64, 1024), (16, 64, 1024)])
+def test_many_lists(colimoe, T, H, E):
+    # more lists than a block of the gather has threads, up to the most
+    c = F.Case(H, 64, E, 2, 1, T, seed=T)
+    assert int(c.lst[1]) > 256 or T == 16
+    c.check_gate_up()
+    c.check_down()
+
+
 @pytest.mark.parametrize("T,H", LIST_SIZES)
 @pytest.mark.parametrize("where", ["one list", "two lists"])
 def test_a_position_named_twice_is_flagged(colimoe, T, H, where):
@@ -401,3 +410,29 @@ def test_two_graphs_on_one_workspace_in_every_kernel(colimoe, T, H, I, E):
             graphs[i].replay()
         assert torch.equal(c.hq, want[0]) and torch.equal(c.hs, want[1]) and torch.equal(c.y[:T], want[2][:T])
     assert B.coli_moe_read_status(c.ws) == (B.COLI_OK, 0)
+
+
+@pytest.mark.parametrize("T,H", LIST_SIZES)
+def test_two_streams_in_every_kernel(colimoe, T, H):
+    # two layers at once, each with its workspace on a stream of its own
+    layers, want = [F.Case(H, 320, 6, 2, 1, T, seed=20 + i) for i in range(2)], []
+    args = []
+    for c in layers:
+        w, xq, xs, res = c.w.cuda(), c.xq.cuda(), c.xs.cuda(), c.res.cuda()
+        args.append((w, xq, xs, res, torch.cuda.Stream()))
+
+    def run(c, a, stream):
+        w, xq, xs, res, _ = a
+        B.check(B.coli_moe_forward_fp8(c.dims, c.weights, xq, xs, T, w, *c.dl, res, c.y, c.ws, stream=stream))
+
+    for c, a in zip(layers, args):
+        run(c, a, None)
+        want.append(c.y[:T].clone())
+        c.y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, a in zip(layers, args):
+            run(c, a, a[4])
+    torch.cuda.synchronize()
+    for c, y in zip(layers, want):
+        assert torch.equal(c.y[:T], y) and B.coli_moe_read_status(c.ws) == (B.COLI_OK, 0)
